@@ -54,6 +54,13 @@ typedef struct CUstream_st *wan_stream_t;
 #define WAN_BF16 1
 #define WAN_FP8  2   /* block mode: FP8 GEMMs, bf16 everything else (see wan_dims) */
 #define WAN_FP8_ATTN 3  /* block mode: WAN_FP8 plus the 8-bit self-attention      */
+/* In wan_rmsnorm and wan_linear WAN_FP8 is an element type: uint8 e4m3 codes with float32 scales. */
+
+/* activations of wan_linear */
+#define WAN_ACT_NONE      0
+#define WAN_ACT_GELU_TANH 1   /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define WAN_ACT_SILU      2   /* z / (1 + exp(-z))                               */
+#define WAN_ACT_RELU      3   /* max(z, 0)                                       */
 
 /* Problem statement of one block call ([WALK]: grid sizes after the (1,2,2)
  * patch embedding, dim, heads, ffn_dim, text length, eps). */
@@ -371,6 +378,65 @@ int wan_quantize_fp8(const void *src, int src_dtype, int rows, int cols, int per
 int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, const uint8_t *w,
                    const float *w_scale, const void *bias, float *out, wan_stream_t stream);
 
+/* wan_linear -- linear layer with bias, activation and residual on the tensor
+ * cores, from one row to many:
+ *   out[m, n] = act(sum_k a[m, k] w[n, k] + bias[n]) + residual[m, n]       (WAN_BF16)
+ *   out[m, n] = act((sum_k a[m, k] w[n, k]) a_scale[m] w_scale[n or 0]
+ *                   + bias[n]) + residual[m, n]                            (WAN_FP8)
+ *   dtype     of a and w: WAN_BF16, or WAN_FP8 (uint8 e4m3 codes as written by
+ *             wan_quantize_fp8 or wan_rmsnorm, [DIGEST] "FP8 GEMM").
+ *   a         [M, K], rows lda elements apart; w [N, K], rows ldw apart. Their
+ *             rows start on 16-byte boundaries (lda and ldw multiples of 8 for
+ *             WAN_BF16, of 16 for WAN_FP8); K itself is free. What lies
+ *             between the rows is not read.
+ *   a_scale   WAN_FP8: float32 [M]; w_scale: float32 [N] with w_scale_rows = 1
+ *             (one per weight row), [1] with w_scale_rows = 0. Ignored for
+ *             WAN_BF16.
+ *   bias      bf16 [N] or NULL.
+ *   activation  WAN_ACT_*.
+ *   residual  [M, N] in res_dtype (WAN_BF16 or WAN_F32), rows ldr apart, added
+ *             after the activation; NULL: none.
+ *   out       [M, N] in out_dtype (WAN_BF16 or WAN_F32), rows ldo apart. May
+ *             be the residual itself (same address, type and stride), and
+ *             overlaps nothing else. What lies between its rows stays.
+ * Products are accumulated in float32 on the tensor cores, everything after
+ * them is float32, and the result is rounded once. A stride is ignored where
+ * its matrix has one row. No workspace. M or N = 0 is an empty call.
+ * The first call on a device must come before any stream capture.
+ * Errors: WAN_EINVAL (sizes, NULLs, strides below the width, overlaps),
+ * WAN_EALIGN (pointers, lda, ldw), WAN_EUNSUPPORTED (dtypes, activation). */
+int wan_linear(int M, int N, int K, int dtype, const void *a, long long lda, const float *a_scale,
+               const void *w, long long ldw, const float *w_scale, int w_scale_rows,
+               const void *bias, int activation, const void *residual, int res_dtype, long long ldr,
+               void *out, int out_dtype, long long ldo, wan_stream_t stream);
+
+/* wan_rmsnorm -- RMS norm of every row with the residual's addition, and an
+ * output in e4m3 for the FP8 product that follows it:
+ *   h = x + residual (h = x without one);  h_out = h
+ *   y = h / sqrt(mean(h^2) + eps) * gain
+ *   rows, D   D in 1..16384.
+ *   x         [rows, D] in x_dtype (WAN_BF16 or WAN_F32), rows ldx elements apart.
+ *   residual  [rows, D] in res_dtype (WAN_BF16 or WAN_F32), rows ldr apart, or NULL.
+ *   gain      float32 [D], or NULL (1).
+ *   h_out     [rows, D] in res_dtype, rows ldh apart, or NULL (not stored);
+ *             needs a residual.
+ *   y         [rows, D] in y_dtype, rows ldy apart: WAN_BF16, WAN_F32, or
+ *             WAN_FP8 (uint8 e4m3 codes of y * (448 / amax), amax the row's
+ *             largest |y|: the codes that wan_quantize_fp8 gives for the
+ *             float32 y, per row).
+ *   row_scale float32 [rows], WAN_FP8 only: amax / 448 (a zero row: codes 0,
+ *             scale 0; a row with a NaN or an infinity: scale and codes NaN).
+ *   An output may be exactly an input matrix (same address, element size and
+ *   stride: h_out = residual, y = x, ...), and overlaps nothing else. What
+ *   lies between the rows of an output stays.
+ * h, the sum of squares, y and the scale are float32; the norm takes h before
+ * it is rounded into h_out. rows = 0 is an empty call.
+ * Errors: WAN_EINVAL (sizes, NULLs, strides below D, overlaps), WAN_EALIGN,
+ * WAN_EUNSUPPORTED (D > 16384, dtypes). */
+int wan_rmsnorm(int rows, int D, const void *x, int x_dtype, long long ldx, const void *residual,
+                int res_dtype, long long ldr, const float *gain, float eps, void *h_out, long long ldh,
+                void *y, int y_dtype, long long ldy, float *row_scale, wan_stream_t stream);
+
 /* UniPC multistep sampler for the latent ("Wan2.2 I2V inference trace",
  * section 4 "DIT": the latent update "UniPC: x_noise <- step(v, t, x_noise)";
  * the method of Zhao et al., 2023, "UniPC: A Unified Predictor-Corrector
@@ -485,12 +551,12 @@ int wan_selftest_watchdog(wan_stream_t stream);
  * class, the number of launches and their summed device time in ms. Events
  * are created on first use and reused; at most 65536 launches are recorded.
  * Not thread-safe against concurrent enable/read. */
-#define WAN_K_GEMM_TC      0  /* tensor-core GEMM (any epilogue)              */
+#define WAN_K_GEMM_TC      0  /* tensor-core GEMM (any epilogue), wan_linear  */
 #define WAN_K_GEMM_SIMT    1  /* CUDA-core GEMM                               */
 #define WAN_K_ATTN_SELF    2  /* tensor-core attention, self (block)          */
 #define WAN_K_ATTN_CROSS   3  /* tensor-core attention, cross (block)         */
 #define WAN_K_ATTN_SIMT    4  /* CUDA-core attention                          */
-#define WAN_K_LAYERNORM    5  /* LayerNorm + modulation / affine              */
+#define WAN_K_LAYERNORM    5  /* LayerNorm + modulation / affine, wan_rmsnorm */
 #define WAN_K_QKNORM_ROPE  6  /* q/k RMSNorm and/or 3D RoPE                   */
 #define WAN_K_EULER        7  /* CFG + Euler update                           */
 #define WAN_K_MISC         8  /* modulation combine, RoPE table               */

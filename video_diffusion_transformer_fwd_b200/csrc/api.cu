@@ -4,6 +4,7 @@
 // snippet; "Wan paper deep dive" (charles2530.github.io), "Video DiT and
 // Flow Matching").
 #include "common.cuh"
+#include "linear.cuh"
 
 #include <stdarg.h>
 #include <stdio.h>
@@ -532,6 +533,53 @@ static int check_shard(const wan_dims *dims, int B, int rows, int tok0) {
   return WAN_OK;
 }
 
+// One matrix argument of a call: `rows` rows (0: the call's) of `width`
+// elements, `ld` apart.
+struct Extent {
+  const char *name;
+  const void *p;
+  size_t es;
+  long long ld, width;
+  bool required, output;
+  int rows = 0;
+};
+
+// NULLs, alignment, row strides, and outputs that overlap another argument. An
+// output may be exactly an input (same address, element size and stride: every
+// element is then read before it is written) when `in_place` is NULL or names
+// that input.
+static int check_extents(const char *op, const Extent *e, size_t n, int rows, const char *in_place = nullptr) {
+  const char *hi[8];
+  for (size_t i = 0; i < n; ++i) {
+    hi[i] = nullptr;
+    if (!e[i].p) {
+      if (e[i].required) return set_error(WAN_EINVAL, "%s: %s is NULL", op, e[i].name);
+      continue;
+    }
+    if (!aligned16(e[i].p)) return set_error(WAN_EALIGN, "%s: %s not 16-byte aligned", op, e[i].name);
+    const long long r = e[i].rows ? e[i].rows : rows;
+    if (r > 1 && e[i].ld < e[i].width)
+      return set_error(WAN_EINVAL, "%s: row stride %lld of %s is below its width %lld", op, e[i].ld, e[i].name, e[i].width);
+    if (r > 1 && e[i].ld > LLONG_MAX / 8 / r) return set_error(WAN_EINVAL, "%s: row stride of %s too large", op, e[i].name);
+    hi[i] = static_cast<const char *>(e[i].p) + (size_t)((r - 1) * (r > 1 ? e[i].ld : 0) + e[i].width) * e[i].es;
+  }
+  for (size_t o = 0; o < n; ++o) {
+    if (!e[o].p || !e[o].output) continue;
+    for (size_t i = 0; i < n; ++i) {
+      if (i == o || !e[i].p || (e[i].output && i < o)) continue;
+      const char *a = static_cast<const char *>(e[o].p), *b = static_cast<const char *>(e[i].p);
+      if (!(a < hi[i] && b < hi[o])) continue;
+      const bool same = a == b && e[o].es == e[i].es && (rows == 1 || e[o].ld == e[i].ld) && e[o].width == e[i].width &&
+                        !e[i].output && e[i].rows == 0;
+      if (!same || (in_place && strcmp(in_place, e[i].name)))
+        return set_error(WAN_EINVAL, "%s: %s overlaps %s", op, e[o].name, e[i].name);
+    }
+  }
+  return WAN_OK;
+}
+
+static bool is_float_dtype(int dt) { return dt == WAN_F32 || dt == WAN_BF16; }
+
 }  // namespace wan
 
 using namespace wan;
@@ -682,6 +730,68 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
   if (!gemm_tc_supported(g)) return set_error(WAN_EUNSUPPORTED, "fp8 linear M=%d N=%d K=%d", M, N, K);
   cudaStream_t s = (cudaStream_t)stream;
   return WAN_PROF(WAN_K_GEMM_TC, s, gemm_tc(g, s));
+}
+
+int wan_rmsnorm(int rows, int D, const void *x, int x_dtype, long long ldx, const void *residual, int res_dtype,
+                long long ldr, const float *gain, float eps, void *h_out, long long ldh, void *y, int y_dtype,
+                long long ldy, float *row_scale, wan_stream_t stream) {
+  g_msg[0] = 0;
+  if (rows < 0 || D < 1) return set_error(WAN_EINVAL, "rmsnorm: rows %d, D %d", rows, D);
+  if (D > RMS_MAX_D) return set_error(WAN_EUNSUPPORTED, "rmsnorm: D %d > %d", D, RMS_MAX_D);
+  if (!(eps >= 0.f)) return set_error(WAN_EINVAL, "rmsnorm: eps must be >= 0");
+  if (!is_float_dtype(x_dtype) || (residual && !is_float_dtype(res_dtype)) || (!is_float_dtype(y_dtype) && y_dtype != WAN_FP8))
+    return set_error(WAN_EUNSUPPORTED, "rmsnorm: dtypes x %d residual %d y %d", x_dtype, res_dtype, y_dtype);
+  if (h_out && !residual) return set_error(WAN_EINVAL, "rmsnorm: h_out needs a residual");
+  if (rows == 0) return WAN_OK;
+  const size_t xs = dtype_size(x_dtype), rs = residual ? dtype_size(res_dtype) : 0, ys = y_dtype == WAN_FP8 ? 1 : dtype_size(y_dtype);
+  const Extent ex[] = {{"x", x, xs, ldx, D, true, false}, {"residual", residual, rs, ldr, D, false, false},
+                       {"gain", gain, 4, D, D, false, false, 1}, {"y", y, ys, ldy, D, true, true},
+                       {"h_out", h_out, rs, ldh, D, false, true},
+                       {"row_scale", y_dtype == WAN_FP8 ? row_scale : nullptr, 4, 1, 1, y_dtype == WAN_FP8, true}};
+  int rc = check_extents("rmsnorm", ex, sizeof(ex) / sizeof(ex[0]), rows);
+  if (rc) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  return WAN_PROF(WAN_K_LAYERNORM, s, launch_rmsnorm(rows, D, x, x_dtype, ldx, residual, res_dtype, ldr, gain, eps, h_out,
+                                                     ldh, y, y_dtype, ldy, row_scale, s));
+}
+
+int wan_linear(int M, int N, int K, int dtype, const void *a, long long lda, const float *a_scale, const void *w,
+               long long ldw, const float *w_scale, int w_scale_rows, const void *bias, int activation,
+               const void *residual, int res_dtype, long long ldr, void *out, int out_dtype, long long ldo,
+               wan_stream_t stream) {
+  g_msg[0] = 0;
+  if (M < 0 || N < 0 || K < 1) return set_error(WAN_EINVAL, "linear: M %d N %d K %d", M, N, K);
+  if (dtype != WAN_BF16 && dtype != WAN_FP8) return set_error(WAN_EUNSUPPORTED, "linear: operand dtype %d", dtype);
+  if (!is_float_dtype(out_dtype) || (residual && !is_float_dtype(res_dtype)))
+    return set_error(WAN_EUNSUPPORTED, "linear: dtypes out %d residual %d", out_dtype, res_dtype);
+  if (activation < WAN_ACT_NONE || activation > WAN_ACT_RELU) return set_error(WAN_EUNSUPPORTED, "linear: activation %d", activation);
+  const bool f8 = dtype == WAN_FP8;
+  if (f8 && w_scale_rows != 0 && w_scale_rows != 1) return set_error(WAN_EINVAL, "linear: w_scale_rows must be 0 or 1");
+  if (M == 0 || N == 0) return WAN_OK;
+  if (M > INT_MAX - 512 || N > INT_MAX / 16 || K > INT_MAX - 512) return set_error(WAN_EINVAL, "linear: sizes too large");
+  const size_t es = f8 ? 1 : 2, rs = residual ? dtype_size(res_dtype) : 0, os = dtype_size(out_dtype);
+  // single rows have no stride of their own
+  const long long pad = 16 / (long long)es;
+  if (M == 1) { lda = (K + pad - 1) / pad * pad; ldr = ldo = N; }
+  if (N == 1) ldw = (K + pad - 1) / pad * pad;
+  if (lda % pad || ldw % pad)
+    return set_error(WAN_EALIGN, "linear: the rows of a and w must start on 16-byte boundaries (lda %lld, ldw %lld)", lda, ldw);
+  const Extent ex[] = {{"a", a, es, lda, K, true, false}, {"w", w, es, ldw, K, true, false, N},
+                       {"a_scale", f8 ? a_scale : nullptr, 4, 1, 1, f8, false},
+                       {"w_scale", f8 ? w_scale : nullptr, 4, 1, 1, f8, false, f8 && w_scale_rows ? N : 1},
+                       {"bias", bias, 2, N, N, false, false, 1}, {"residual", residual, rs, ldr, N, false, false},
+                       {"out", out, os, ldo, N, true, true}};
+  int rc = check_extents("linear", ex, sizeof(ex) / sizeof(ex[0]), M, "residual");
+  if (rc) return rc;
+  LinArgs g = {};
+  g.M = M; g.N = N; g.K = K; g.fp8 = f8;
+  g.a = a; g.lda = lda; g.a_scale = a_scale;
+  g.w = w; g.ldw = ldw; g.w_scale = w_scale; g.w_scale_rows = w_scale_rows;
+  g.bias = bias; g.act = activation;
+  g.res = residual; g.res_f32 = res_dtype == WAN_F32; g.ldr = ldr;
+  g.out = out; g.out_f32 = out_dtype == WAN_F32; g.ldo = ldo;
+  cudaStream_t s = (cudaStream_t)stream;
+  return WAN_PROF(WAN_K_GEMM_TC, s, launch_linear(g, s));
 }
 
 size_t wan_attention_8bit_workspace_bytes(int B, int heads, int Lq, int Lk) {

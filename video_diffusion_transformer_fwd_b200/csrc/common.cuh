@@ -231,6 +231,12 @@ int launch_rope_only(void *p, int dtype, int rows, int ld, int D, int head_dim,
 // S = sum of the `parts` partial sums at ss[r * ss_stride + 0 .. parts-1].
 int launch_scale_rows(void *p, int rows, int ld, int D, const float *ss, int ss_stride, int parts,
                       float eps, cudaStream_t s);
+// y = RMSNorm(x + r) * g, h = x + r (rmsnorm.cu); r, g, h may be NULL; y_dtype
+// WAN_FP8: e4m3 codes and one scale per row. Row strides in elements.
+int launch_rmsnorm(int rows, int D, const void *x, int x_dtype, long long ldx, const void *r, int res_dtype,
+                   long long ldr, const float *g, float eps, void *h, long long ldh, void *y, int y_dtype,
+                   long long ldy, float *scale, cudaStream_t s);
+constexpr int RMS_MAX_D = 16384;
 int launch_rope_table(int head_dim, int max_pos, double theta, float *table, cudaStream_t s);
 // dst = src with its chunk axes permuted: src is [dims[0]] ... [dims[nd-1]]
 // chunks of chunk_bytes, dst axis k runs over src axis perm[k].

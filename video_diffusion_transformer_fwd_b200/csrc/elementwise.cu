@@ -7,8 +7,8 @@
 // snippet (classifier-free guidance); "Wan paper deep dive"
 // (charles2530.github.io), "Video DiT and Flow Matching" (Euler in sigma).
 #include "common.cuh"
+#include "e4m3.cuh"
 
-#include <cuda_fp8.h>
 #include <math.h>
 
 namespace wan {
@@ -42,23 +42,6 @@ int launch_mod_combine(const float *modulation, const float *e0, float *mod, int
 // x * (448 / amax), ties to even, clamped to +-448; both factors and the
 // product are rounded to fp32 as formed. An all-zero row gets scale 0.
 // ----------------------------------------------------------------------------
-constexpr float E4M3_MAX = 448.f;
-
-// four values -> four e4m3 bytes, the first in the lowest byte
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
-}
-
-__device__ __forceinline__ float e4m3_inv_scale(float amax) {
-  return amax > 0.f ? __fdiv_rn(E4M3_MAX, amax) : 0.f;
-}
-
-__device__ __forceinline__ float absmax4(float4 v) {
-  return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-}
-
 __device__ __forceinline__ float block_max(float v, float *red) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int nw = (blockDim.x + 31) >> 5;
@@ -71,10 +54,6 @@ __device__ __forceinline__ float block_max(float v, float *red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
   return t;
-}
-
-__device__ __forceinline__ uint32_t quant4(float4 v, float inv) {
-  return e4m3x4(__fmul_rn(v.x, inv), __fmul_rn(v.y, inv), __fmul_rn(v.z, inv), __fmul_rn(v.w, inv));
 }
 
 // One CTA per row of src (row stride ld elements): codes [rows, cols], scale [rows].

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(PKG, "libwan.so")
 
 WAN_OK, WAN_EINVAL, WAN_EALIGN, WAN_EUNSUPPORTED, WAN_ECUDA, WAN_ETIMEOUT, WAN_EBOUNDS = 0, -1, -2, -3, -4, -5, -6
 WAN_F32, WAN_BF16, WAN_FP8, WAN_FP8_ATTN = 0, 1, 2, 3
+WAN_ACT_NONE, WAN_ACT_GELU_TANH, WAN_ACT_SILU, WAN_ACT_RELU = range(4)
 WAN_NOALLOC_WORKSPACE_BYTES = 16 << 20
 (WAN_WS_ACT, WAN_WS_QKV, WAN_WS_O, WAN_WS_QC, WAN_WS_KVC, WAN_WS_OC, WAN_WS_H, WAN_WS_MOD,
  WAN_WS_STATS, WAN_WS_A8, WAN_WS_ASCALE, WAN_WS_ATTN8) = range(12)
@@ -69,7 +70,7 @@ class wan_model_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in MODEL_WEIGHT_FIELDS]
 
 
-_c_int, _vp, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_c_int, _vp, _sz, _ll = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong
 
 _SIGS = {
     "wan_last_error": (ctypes.c_char_p, []),
@@ -99,6 +100,10 @@ _SIGS = {
     "wan_model_workspace_bytes": (_sz, [ctypes.POINTER(wan_model_dims), _c_int]),
     "wan_quantize_fp8": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "wan_linear_fp8": (_c_int, [_c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "wan_linear": (_c_int, [_c_int, _c_int, _c_int, _c_int, _vp, _ll, _vp, _vp, _ll, _vp, _c_int, _vp, _c_int, _vp,
+                            _c_int, _ll, _vp, _c_int, _ll, _vp]),
+    "wan_rmsnorm": (_c_int, [_c_int, _c_int, _vp, _c_int, _ll, _vp, _c_int, _ll, _vp, ctypes.c_float, _vp, _ll, _vp,
+                             _c_int, _ll, _vp, _vp]),
     "wan_attention_8bit_workspace_bytes": (_sz, [_c_int, _c_int, _c_int, _c_int]),
     "wan_unipc_coefficients": (_c_int, [ctypes.POINTER(ctypes.c_double), _c_int, _c_int, _c_int, _c_int,
                                         ctypes.POINTER(ctypes.c_double)]),
@@ -225,6 +230,18 @@ def wan_linear_fp8(M, N, K, a, a_scale, w, w_scale, bias, out, stream):
     return load().wan_linear_fp8(M, N, K, a, a_scale, w, w_scale, bias, out, stream)
 
 
+def wan_linear(M, N, K, dtype, a, lda, a_scale, w, ldw, w_scale, w_scale_rows, bias, activation, residual, res_dtype,
+               ldr, out, out_dtype, ldo, stream):
+    return load().wan_linear(M, N, K, dtype, a, lda, a_scale, w, ldw, w_scale, w_scale_rows, bias, activation,
+                             residual, res_dtype, ldr, out, out_dtype, ldo, stream)
+
+
+def wan_rmsnorm(rows, D, x, x_dtype, ldx, residual, res_dtype, ldr, gain, eps, h_out, ldh, y, y_dtype, ldy, row_scale,
+                stream):
+    return load().wan_rmsnorm(rows, D, x, x_dtype, ldx, residual, res_dtype, ldr, gain, eps, h_out, ldh, y, y_dtype,
+                              ldy, row_scale, stream)
+
+
 def wan_attention_8bit_workspace_bytes(B, heads, Lq, Lk):
     return load().wan_attention_8bit_workspace_bytes(B, heads, Lq, Lk)
 
@@ -343,6 +360,168 @@ def linear_fp8(a, a_scale, w, w_scale, bias=None, out=None, stream=None):
         out = torch.empty((M, N), dtype=torch.float32, device=a.device)
     check(wan_linear_fp8(M, N, K, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
                          _ptr(bias), out.data_ptr(), _stream(stream)))
+    return out
+
+
+ACTIVATIONS = {"none": WAN_ACT_NONE, "gelu_tanh": WAN_ACT_GELU_TANH, "silu": WAN_ACT_SILU, "relu": WAN_ACT_RELU}
+
+
+def _elem_code(t) -> int:
+    """dtype_code, and WAN_FP8 for e4m3 codes (uint8 or float8_e4m3fn)."""
+    torch = _torch()
+    if t.dtype == torch.uint8 or t.dtype == torch.float8_e4m3fn:
+        return WAN_FP8
+    return dtype_code(t)
+
+
+def _rows(t, name):
+    """t as a matrix of its last axis (a view) and its row stride in elements."""
+    m = t if t.dim() == 2 else t.view(-1, t.shape[-1])
+    rows, cols = m.shape
+    if cols > 1 and m.stride(1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    ld = m.stride(0) if rows > 1 else cols
+    return m, ld
+
+
+def _one_device(**tensors):
+    """Index of the CUDA device that holds every tensor given."""
+    idx = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} is not on a CUDA device")
+        if idx is None:
+            idx = d
+        elif d != idx:
+            raise ValueError(f"{name} is on cuda:{d}, the other tensors on cuda:{idx}")
+    return idx
+
+
+def _vector(t, name, n, dtype):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+
+
+def _empty_on(stream, shape, dtype, device):
+    """torch.empty whose memory belongs to the stream that writes it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row_scale=None, h_out=None, stream=None):
+    """RMS norm over the last axis with the residual's addition (wan_rmsnorm):
+    h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain.
+
+    x [..., D] and residual [..., D] are bf16 or float32, gain float32 [D].
+    ``out_dtype`` is "bf16", "f32" or "fp8" (e4m3 codes, uint8, with one
+    float32 scale per row); by default the type of ``out``, or of x. Outputs
+    that are not given are allocated. Rows may be strided (2-D tensors).
+    Returns (y, row_scale, h): row_scale is None unless y holds codes, h is x
+    itself without a residual and has the residual's type with one."""
+    torch = _torch()
+    dev = _one_device(x=x, gain=gain, residual=residual, out=out, row_scale=row_scale, h_out=h_out)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rmsnorm(x, gain, residual, eps, out_dtype, out, row_scale, h_out, stream)
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x needs a last axis to normalise")
+    code = (_elem_code(out) if out is not None else dtype_code(x)) if out_dtype is None else DTYPE_CODES[out_dtype]
+    if out is None:
+        out = _empty_on(stream, x.shape, {WAN_FP8: torch.uint8, WAN_BF16: torch.bfloat16, WAN_F32: torch.float32}[code],
+                        x.device)
+    elif _elem_code(out) != code:
+        raise ValueError(f"out has type {out.dtype}, not {out_dtype}")
+    xm, ldx = _rows(x, "x")
+    ym, ldy = _rows(out, "out")
+    rows, D = xm.shape
+    if out.shape != x.shape or (residual is not None and residual.shape != x.shape) or \
+            (h_out is not None and h_out.shape != x.shape):
+        raise ValueError("x, residual, out and h_out must have one shape")
+    if gain is not None:
+        _vector(gain, "gain", D, torch.float32)
+    if code == WAN_FP8:
+        if row_scale is None:
+            row_scale = _empty_on(stream, x.shape[:-1], torch.float32, x.device)
+        _vector(row_scale, "row_scale", rows, torch.float32)
+    elif row_scale is not None:
+        raise ValueError("row_scale goes with e4m3 codes")
+    rcode, rm, ldr, hm, ldh = WAN_F32, None, 0, None, 0
+    if residual is not None:
+        rcode = dtype_code(residual)
+        rm, ldr = _rows(residual, "residual")
+        if h_out is None:
+            h_out = _empty_on(stream, x.shape, residual.dtype, x.device)
+        elif h_out.dtype != residual.dtype:
+            raise ValueError("h_out has the residual's type")
+        hm, ldh = _rows(h_out, "h_out")
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual")
+    check(wan_rmsnorm(rows, D, xm.data_ptr(), dtype_code(x), ldx, _ptr(rm), rcode, ldr, _ptr(gain), eps, _ptr(hm), ldh,
+                      ym.data_ptr(), code, ldy, _ptr(row_scale), _stream(stream)))
+    return out, row_scale, (x if residual is None else h_out)
+
+
+def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_scale=None, out=None, out_dtype=None,
+           stream=None):
+    """Linear layer with bias, activation and residual (wan_linear):
+    act(a w^T [a_scale w_scale] + bias) + residual, from one row to many.
+
+    a [..., K] and w [N, K] are bf16, or e4m3 codes (uint8 or float8_e4m3fn)
+    with float32 scales: a_scale one per row of a, w_scale one for w or one
+    per row of w. bias is bf16 [N]; ``activation`` "none", "gelu_tanh", "silu"
+    or "relu"; residual [..., N] bf16 or float32 and may be ``out`` itself.
+    ``out_dtype`` is "bf16" or "f32" (by default the type of ``out``, of the
+    residual, or bf16). Rows may be strided (2-D tensors); those of a and w
+    start on 16-byte boundaries. Returns out [..., N]."""
+    torch = _torch()
+    dev = _one_device(a=a, w=w, bias=bias, residual=residual, a_scale=a_scale, w_scale=w_scale, out=out)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return linear(a, w, bias, activation, residual, a_scale, w_scale, out, out_dtype, stream)
+    code = _elem_code(a)
+    if _elem_code(w) != code:
+        raise ValueError(f"a has type {a.dtype}, w {w.dtype}")
+    if w.dim() != 2 or a.dim() == 0 or a.shape[-1] != w.shape[1]:
+        raise ValueError(f"a {tuple(a.shape)} does not fit w {tuple(w.shape)}")
+    N, K = w.shape
+    shape = a.shape[:-1] + (N,)
+    if out is None:
+        dt = {"bf16": torch.bfloat16, "f32": torch.float32, None: torch.bfloat16 if residual is None else residual.dtype}[out_dtype]
+        out = _empty_on(stream, shape, dt, a.device)
+    elif out_dtype is not None and dtype_code(out) != DTYPE_CODES[out_dtype]:
+        raise ValueError(f"out has type {out.dtype}, not {out_dtype}")
+    if out.shape != shape or (residual is not None and residual.shape != shape):
+        raise ValueError(f"out and residual must have shape {tuple(shape)}")
+    if N == 0:
+        return out
+    am, lda = _rows(a, "a")
+    wm, ldw = _rows(w, "w")
+    om, ldo = _rows(out, "out")
+    M = am.shape[0]
+    rows = 0
+    if code == WAN_FP8:
+        if a_scale is None or w_scale is None:
+            raise ValueError("e4m3 operands need a_scale and w_scale")
+        rows = 1 if w_scale.numel() == N and N > 1 else 0
+        _vector(a_scale, "a_scale", M, torch.float32)
+        _vector(w_scale, "w_scale", N if rows else 1, torch.float32)
+    elif a_scale is not None or w_scale is not None:
+        raise ValueError("bf16 operands have no scales")
+    if bias is not None:
+        _vector(bias, "bias", N, torch.bfloat16)
+    rcode, rm, ldr = WAN_F32, None, 0
+    if residual is not None:
+        rcode = dtype_code(residual)
+        rm, ldr = _rows(residual, "residual")
+    check(wan_linear(M, N, K, code, am.data_ptr(), lda, _ptr(a_scale), wm.data_ptr(), ldw, _ptr(w_scale), rows,
+                     _ptr(bias), ACTIVATIONS[activation], _ptr(rm), rcode, ldr, om.data_ptr(), dtype_code(out), ldo,
+                     _stream(stream)))
     return out
 
 
