@@ -772,7 +772,7 @@ int wan_linear(int M, int N, int K, int dtype, const void *a, long long lda, con
   const size_t es = f8 ? 1 : 2, rs = residual ? dtype_size(res_dtype) : 0, os = dtype_size(out_dtype);
   // single rows have no stride of their own
   const long long pad = 16 / (long long)es;
-  if (M == 1) { lda = (K + pad - 1) / pad * pad; ldr = ldo = N; }
+  if (M == 1) { lda = (K + pad - 1) / pad * pad; ldr = ldo = (N + 7LL) / 8 * 8; }
   if (N == 1) ldw = (K + pad - 1) / pad * pad;
   if (lda % pad || ldw % pad)
     return set_error(WAN_EALIGN, "linear: the rows of a and w must start on 16-byte boundaries (lda %lld, ldw %lld)", lda, ldw);

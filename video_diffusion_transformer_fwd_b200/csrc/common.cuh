@@ -119,7 +119,7 @@ inline size_t dtype_size(int dt) { return dt == WAN_F32 ? 4 : 2; }   // WAN_FP8:
 
 // ---------------------------------------------------------------- internal kernels API
 
-enum Epilogue { EPI_STORE = 0, EPI_GELU = 1, EPI_RESID = 2, EPI_QKNORM = 3, EPI_SILU = 4 };
+enum Epilogue { EPI_STORE = 0, EPI_GELU = 1, EPI_RESID = 2, EPI_QKNORM = 3, EPI_SILU = 4, EPI_LINEAR = 5 };
 
 // C = A B^T (+ bias) with a fused epilogue. A [M,K] row-major (lda),
 // B given as up to 3 row-major segments [segN, K] (ldb = K) stacked along N,
@@ -137,6 +137,7 @@ enum Epilogue { EPI_STORE = 0, EPI_GELU = 1, EPI_RESID = 2, EPI_QKNORM = 3, EPI_
 //              tok0 + m % rows_per_seq when
 //              bit s of rope_mask is set; otherwise C = y. The row's RMS factor
 //              is applied later (attention logit scale for q, a row pass for k).
+//   EPI_LINEAR: wan_linear (linear.cuh; gemm_tc_linear)
 struct GemmArgs {
   int M, N, K;
   const void *A; int lda;

@@ -37,7 +37,10 @@
 // Tiles are walked in groups of 8 M-tiles (2048 rows) so a wave of pairs
 // shares A and B panels in L2. Every wait is bounded (sm100::mbar_wait).
 #include "common.cuh"
+#include "linear.cuh"
 #include "sm100.cuh"
+
+#include <atomic>
 
 namespace wan {
 
@@ -55,20 +58,23 @@ constexpr int BK8 = 128;                 // e4m3 elements per stage row (128 byt
 constexpr int STG_BYTES = 32 * 32 * 4;  // one warp's 32 x 32 fp32 staging tile (128-byte swizzle)
 constexpr bool USE_WIDE = true;          // 256 x 512 tiles wherever the shape allows
 
-// Tile geometry of the two variants.
-template <bool WIDE>
+// Tile geometry of the two variants. LIN (wan_linear): the narrow tile with
+// twice the epilogue warps, each on 128 columns with two staging tiles.
+template <bool WIDE, bool LIN = false>
 struct Geo {
   static constexpr int BN = WIDE ? 512 : 256;              // output columns per pair tile
-  static constexpr int STAGES = WIDE ? 4 : 6;
+  static constexpr int STAGES = WIDE ? 4 : LIN ? 5 : 6;
   static constexpr int B_BYTES = (BN / 2) * BK * 2;        // this CTA's half of B
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int EPI_WARPS = WIDE ? 8 : 4;
+  static constexpr int EPI_WARPS = (WIDE ? 8 : 4) * (LIN ? 2 : 1);
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int NACC = WIDE ? 1 : 2;                // TMEM accumulators (BN columns each)
   static constexpr int NSTG = WIDE ? 1 : 2;                // residual staging tiles per epilogue warp
   static constexpr int EPI_SMEM = EPI_WARPS * NSTG * STG_BYTES;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_SMEM + 256;
+  static_assert(!(WIDE && LIN), "wan_linear runs the narrow tile");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+  static_assert(8 * (2 * STAGES + 4) + 16 + 8 * EPI_WARPS <= 256, "barriers");
   static_assert(NACC * BN <= (int)TMEM_COLS, "TMEM columns");
 };
 
@@ -86,6 +92,7 @@ struct TcParams {
   const float *rope; int rope_mask; int rope_vec; int L, H, W; int head_dim; int tok0;   // L: rows per sequence
   int *watchdog;
   const void *ss_hi; int *dbg;            // debug bounds checks: end of ss
+  LinEpilogue lin;                        // EPI_LINEAR
 };
 
 __device__ __forceinline__ void tile_coords(int t, const TcParams &p, int &mb, int &nb) {
@@ -112,12 +119,235 @@ __device__ __forceinline__ float bf16_bits_to_float(uint32_t lo16) {
   return __uint_as_float(lo16 << 16);
 }
 
+// wan_linear's epilogue: warp `ew` of 8 takes 128 columns of 32 rows of every
+// tile of its pair, 32 columns at a time, one thread per row: scales, bias,
+// activation, residual, output. Residual and output pass through two 4 KB
+// shared-memory tiles of the warp (128-byte rows of 32 float32 or 64 bf16,
+// 16-byte group g of row r at g ^ (r & 7)) and the TMA unit, which keeps the
+// warp's own loads and stores to shared memory: a version that stored rows of
+// 32 bytes from registers held the 7800 x 8960 x 1536 product at 182 us, its
+// products alone take 141 us. The residual of a chunk is asked for when the
+// chunk before it has been added, the first one of a tile during the last of
+// the tile before. Outputs (or residuals) whose rows do not start on 16-byte
+// boundaries are turned around in shared memory instead and stored a column
+// per lane.
+template <bool F8>
+struct LinearEpilogue {
+  using G = Geo<false, true>;
+  const TcParams &p;
+  const LinEpilogue &e;
+  const CUtensorMap *tmX, *tmR;
+  uint8_t *tiles;               // this warp's two staging tiles
+  uint32_t rbar;                // counts the bytes of a residual tile
+  volatile int *abort_flag;
+  int hcol, q, lane, rank, pair, npairs;
+  bool tma_res;
+  // the residual tile asked for last: pair tile rt, unit ru (units of 128 bytes a row)
+  int rt, ru, asked = 0, taken = 0;
+
+  __device__ __forceinline__ int res_cols() const { return e.res_f32 ? 32 : 64; }
+  __device__ __forceinline__ void corner(int t, int &m0, int &n0) const {
+    int mb, nb;
+    tile_coords(t, p, mb, nb);
+    m0 = mb * 2 * BM + rank * BM + q * 32;
+    n0 = nb * G::BN + hcol;
+  }
+  // ask for the residual unit after (rt, ru); units outside the matrix are passed over
+  __device__ __forceinline__ void ask_next() {
+    int m0, n0;
+    for (++ru; rt < p.num_tiles; rt += npairs, ru = 0) {
+      corner(rt, m0, n0);
+      if (m0 < p.M && n0 + ru * res_cols() < p.N && ru * res_cols() < 128) break;
+    }
+    if (rt >= p.num_tiles) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(rbar, STG_BYTES);
+      tma_load_2d(smem_u32(tiles), tmR, n0 + ru * res_cols(), m0, rbar);
+    }
+    ++asked;
+  }
+  __device__ __forceinline__ uint8_t *slot(uint8_t *tile, int row, int g) const {
+    return tile + row * 128 + ((g ^ (row & 7)) << 4);
+  }
+
+  // v += the residual of chunk c
+  __device__ __forceinline__ bool add_residual(float (&v)[32], int c, bool last) {
+    const bool fresh = e.res_f32 || !(c & 1);
+    if (fresh) {
+      const bool ok = mbar_wait(rbar, taken & 1, abort_flag, p.watchdog, 0x123);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      ++taken;
+    }
+    if (e.res_f32) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float4 x = *reinterpret_cast<const float4 *>(slot(tiles, lane, g));
+        v[4 * g] += x.x; v[4 * g + 1] += x.y; v[4 * g + 2] += x.z; v[4 * g + 3] += x.w;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(slot(tiles, lane, 4 * (c & 1) + g));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[8 * g + 2 * k] += bf16_bits_to_float(w[k] & 0xFFFFu);
+          v[8 * g + 2 * k + 1] += bf16_bits_to_float(w[k] >> 16);
+        }
+      }
+    }
+    __syncwarp();                                // the tile has been read
+    if (e.res_f32 || (c & 1) || last) ask_next();
+    return true;
+  }
+
+  // rows that the TMA unit cannot address: column `lane` of the chunk, row by row
+  __device__ __forceinline__ void store_by_columns(const float (&v)[32], int m0, int n) {
+    uint8_t *tile = tiles + STG_BYTES;
+    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      *reinterpret_cast<float4 *>(slot(tile, lane, g)) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+    __syncwarp();
+    if (n + lane >= p.N) return;
+    const int rows = min(32, p.M - m0);
+    const bool res = e.res && !tma_res;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) {
+      float o = *reinterpret_cast<const float *>(slot(tile, r, lane >> 2) + 4 * (lane & 3));
+      if (res) o += lin_res(e, m0 + r, n + lane);
+      lin_put(e, m0 + r, n + lane, o);
+    }
+  }
+
+  // returns when all tiles are done, or a wait gave up
+  __device__ __forceinline__ void run(uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty) {
+    const uint32_t free0 = mapa_shared(smem_u32(&tempty[0]), 0), free1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    const bool tma_out = e.vec_out;
+    tma_res = e.res && e.vec_res;
+    int stores = 0;
+    rt = pair; ru = -1;
+    if (tma_res) ask_next();
+    int i = 0;
+    for (int t = pair; t < p.num_tiles; t += npairs, ++i) {
+      const int buf = i & 1;
+      int m0, n0;
+      corner(t, m0, n0);
+      const int m = m0 + lane;
+      // Per-column operands, read while the tile's products run: lane l holds
+      // columns 8 (l % 16) .. + 7 of the warp's 128, taken by shuffles.
+      const int c0 = n0 + 8 * (lane & 15);
+      uint4 bias8 = make_uint4(0u, 0u, 0u, 0u);
+      float4 s_lo = make_float4(1.f, 1.f, 1.f, 1.f), s_hi = s_lo;
+      const bool rows = F8 && e.w_scale_rows;
+      if (c0 + 8 <= p.N) {
+        if (e.bias) bias8 = *reinterpret_cast<const uint4 *>(e.bias + c0);
+        if (rows) { s_lo = load4(e.w_scale + c0); s_hi = load4(e.w_scale + c0 + 4); }
+      } else if (c0 < p.N) {                     // the last group is short
+        uint32_t b[8];
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          b[j] = e.bias && c0 + j < p.N ? __bfloat16_as_ushort(e.bias[c0 + j]) : 0u;
+          f[j] = rows && c0 + j < p.N ? e.w_scale[c0 + j] : 1.f;
+        }
+        bias8 = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+        s_lo = make_float4(f[0], f[1], f[2], f[3]);
+        s_hi = make_float4(f[4], f[5], f[6], f[7]);
+      }
+      float rs = 1.f;
+      if (F8) {
+        rs = m < p.M ? e.a_scale[m] : 0.f;
+        if (!rows) rs *= e.w_scale[0];
+      }
+      const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i >> 1) & 1, abort_flag, p.watchdog, 0x122);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + buf * G::BN + hcol + c * 32, r);
+        tmem_ld_wait();
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(buf ? free1 : free0);
+        }
+        const int n = n0 + c * 32;
+        if (m0 >= p.M || n >= p.N) continue;     // warp-uniform
+        const bool last = c == 3 || n + 32 >= p.N;
+        float v[32];
+#pragma unroll
+        for (int j4 = 0; j4 < 4; ++j4) {         // columns 8 j4 .. of the chunk: lane 4 c + j4
+          const int src = 4 * c + j4;
+          const uint32_t w[4] = {__shfl_sync(0xffffffffu, bias8.x, src), __shfl_sync(0xffffffffu, bias8.y, src),
+                                 __shfl_sync(0xffffffffu, bias8.z, src), __shfl_sync(0xffffffffu, bias8.w, src)};
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = rs;
+          if (rows) {
+            f[0] *= __shfl_sync(0xffffffffu, s_lo.x, src); f[1] *= __shfl_sync(0xffffffffu, s_lo.y, src);
+            f[2] *= __shfl_sync(0xffffffffu, s_lo.z, src); f[3] *= __shfl_sync(0xffffffffu, s_lo.w, src);
+            f[4] *= __shfl_sync(0xffffffffu, s_hi.x, src); f[5] *= __shfl_sync(0xffffffffu, s_hi.y, src);
+            f[6] *= __shfl_sync(0xffffffffu, s_hi.z, src); f[7] *= __shfl_sync(0xffffffffu, s_hi.w, src);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float b = (k & 1) ? __uint_as_float(w[k >> 1] & 0xFFFF0000u) : __uint_as_float(w[k >> 1] << 16);
+            const float acc = __uint_as_float(r[8 * j4 + k]);
+            v[8 * j4 + k] = F8 ? fmaf(acc, f[k], b) : acc + b;
+          }
+        }
+        lin_act_row(v, e.act);
+        if (tma_res && !add_residual(v, c, last)) return;
+        if (!tma_out || (e.res && !tma_res)) { store_by_columns(v, m0, n); continue; }
+        // with a residual the second tile alone holds the output, else both in turn
+        uint8_t *tile = tiles + (e.res || (stores & 1) ? STG_BYTES : 0);
+        if (e.out_f32 || !(c & 1)) {
+          if (lane == 0) {                       // this tile's previous store has read it
+            if (e.res) bulk_wait_group_read<0>(); else bulk_wait_group_read<1>();
+          }
+          __syncwarp();
+        }
+        if (e.out_f32) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            *reinterpret_cast<float4 *>(slot(tile, lane, g)) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(v[8 * g], v[8 * g + 1]),
+                                         __floats2bfloat162_rn(v[8 * g + 2], v[8 * g + 3]),
+                                         __floats2bfloat162_rn(v[8 * g + 4], v[8 * g + 5]),
+                                         __floats2bfloat162_rn(v[8 * g + 6], v[8 * g + 7])};
+            *reinterpret_cast<uint4 *>(slot(tile, lane, 4 * (c & 1) + g)) = *reinterpret_cast<const uint4 *>(h);
+          }
+        }
+        if (e.out_f32 || (c & 1) || last) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(tmX, smem_u32(tile), e.out_f32 ? n : n0 + (c & ~1) * 32, m0);
+            bulk_commit_group();
+          }
+          ++stores;
+        }
+      }
+    }
+  }
+  // a residual tile still in flight (after a wait gave up) lands before the CTA ends
+  __device__ __forceinline__ void drain() {
+    int never = 0;
+    if (tma_res && taken < asked) mbar_wait(rbar, taken & 1, &never, p.watchdog, 0x124);
+  }
+};
+
 template <int EPI, bool F8, bool WIDE>
-__global__ void __launch_bounds__(Geo<WIDE>::THREADS, 1)
+__global__ void __launch_bounds__(Geo<WIDE, EPI == EPI_LINEAR>::THREADS, 1)
 gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmB2,
                const __grid_constant__ CUtensorMap tmX, const TcParams p) {
-  using G = Geo<WIDE>;
+  using G = Geo<WIDE, EPI == EPI_LINEAR>;
   constexpr int BN = G::BN, STAGES = G::STAGES, B_BYTES = G::B_BYTES, STAGE_BYTES = G::STAGE_BYTES;
   constexpr int NACC = G::NACC, NSTG = G::NSTG;
   extern __shared__ uint8_t smem_raw[];
@@ -130,6 +360,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 4);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile uint32_t *skip = reinterpret_cast<volatile uint32_t *>(tmem_slot + 2);
+  uint64_t *rbars = reinterpret_cast<uint64_t *>(tmem_slot + 4);     // EPI_LINEAR: one per epilogue warp
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -158,6 +389,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       mbar_init(smem_u32(&tfull[b]), 1);
       mbar_init(smem_u32(&tempty[b]), 2 * G::EPI_WARPS);
     }
+    if (EPI == EPI_LINEAR)
+      for (int w = 0; w < G::EPI_WARPS; ++w) mbar_init(smem_u32(&rbars[w]), 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
@@ -257,6 +490,14 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           tc_commit_pair(mapa_shared(fb, 1));
         }
       }
+    }
+  } else if (EPI == EPI_LINEAR) {
+    if constexpr (EPI == EPI_LINEAR) {
+      const int ew = warp - 2;
+      LinearEpilogue<F8> le{p, p.lin, &tmX, &tmB1, sE + ew * NSTG * STG_BYTES, smem_u32(&rbars[ew]), abort_flag,
+                            128 * (ew >> 2), warp & 3, lane, (int)rank, pair, npairs};
+      le.run(tmem_base, tfull, tempty);
+      le.drain();
     }
   } else {
     // ------------------------------------------------ epilogue (warps 2.., both CTAs)
@@ -509,8 +750,11 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 template <int EPI, bool F8, bool WIDE>
 int launch(const CUtensorMap &ta, const CUtensorMap *tb, const CUtensorMap &tx, const TcParams &p,
            cudaStream_t s) {
-  using G = Geo<WIDE>;
-  static int max_pairs = 0;         // per process; the attribute is per function
+  using G = Geo<WIDE, EPI == EPI_LINEAR>;
+  static std::atomic<int> known[64];    // CTA pairs that fit, per device (0: not asked yet); the attribute is per device too
+  int dev = 0;
+  WAN_TRY_CUDA(cudaGetDevice(&dev), "gemm_tc device");
+  int max_pairs = dev < 64 ? known[dev].load() : 0;
   if (!max_pairs) {
     WAN_TRY_CUDA(cudaFuncSetAttribute(gemm_tc_kernel<EPI, F8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       G::SMEM_BYTES), "gemm_tc smem attribute");
@@ -526,6 +770,7 @@ int launch(const CUtensorMap &ta, const CUtensorMap *tb, const CUtensorMap &tx, 
     int clusters = 0;
     WAN_TRY_CUDA(cudaOccupancyMaxActiveClusters(&clusters, gemm_tc_kernel<EPI, F8, WIDE>, &qc), "gemm_tc occupancy");
     max_pairs = clusters > 0 ? clusters : sm_count() / 2;
+    if (dev < 64) known[dev].store(max_pairs);
   }
   const int pairs = p.num_tiles < max_pairs ? p.num_tiles : max_pairs;
   cudaLaunchConfig_t cfg = {};
@@ -554,6 +799,41 @@ int launch_epi(int epi, const CUtensorMap &ta, const CUtensorMap *tb, const CUte
   }
 }
 }  // namespace
+
+// wan_linear on CTA pairs: the same products with wan_linear's epilogue. K may
+// end inside a step and N inside a tile (the TMA unit fills zeros).
+int gemm_tc_linear(const LinArgs &g, cudaStream_t s) {
+  CUtensorMap ta, tb[3], tx;
+  const int bk = g.fp8 ? BK8 : BK;
+  int rc;
+  if (g.fp8) {
+    if ((rc = encode_tmap_2d_u8(&ta, g.a, g.K, g.M, (uint64_t)g.lda, BK8, BM))) return rc;
+    if ((rc = encode_tmap_2d_u8(&tb[0], g.w, g.K, g.N, (uint64_t)g.ldw, BK8, 128))) return rc;
+  } else {
+    if ((rc = encode_tmap_2d_bf16(&ta, g.a, g.K, g.M, (uint64_t)g.lda * 2, BK, BM))) return rc;
+    if ((rc = encode_tmap_2d_bf16(&tb[0], g.w, g.K, g.N, (uint64_t)g.ldw * 2, BK, 128))) return rc;
+  }
+  TcParams p = {};
+  p.lin = lin_epilogue(g);
+  tb[1] = tb[2] = tx = tb[0];                     // maps that no copy uses stay valid ones
+  auto rows32 = [&](CUtensorMap *t, const void *base, long long ld, bool f32) {
+    return f32 ? encode_tmap_2d_f32(t, base, g.N, g.M, (uint64_t)ld * 4, 32, 32)
+               : encode_tmap_2d_bf16(t, base, g.N, g.M, (uint64_t)ld * 2, 64, 32);
+  };
+  if (p.lin.vec_out && (rc = rows32(&tx, g.out, g.ldo, g.out_f32))) return rc;
+  if (g.res && p.lin.vec_res && (rc = rows32(&tb[1], g.res, g.ldr, g.res_f32))) return rc;
+  p.M = g.M; p.N = g.N; p.K = g.K;
+  p.segN = (g.N + 255) / 256 * 256;               // one weight segment
+  p.num_m = (g.M + 2 * BM - 1) / (2 * BM);
+  p.num_n = (g.N + 255) / 256;
+  if ((long long)p.num_m * p.num_n > 0x3fffffff) return set_error(WAN_EINVAL, "linear: M=%d N=%d too large", g.M, g.N);
+  p.num_tiles = p.num_m * p.num_n;
+  p.num_k = (g.K + bk - 1) / bk;
+  p.L = p.H = p.W = 1; p.head_dim = 128; p.rows_per_gate = 1;
+  p.watchdog = watchdog_ptr();
+  p.dbg = dbg_word();
+  return g.fp8 ? launch<EPI_LINEAR, true, false>(ta, tb, tx, p, s) : launch<EPI_LINEAR, false, false>(ta, tb, tx, p, s);
+}
 
 bool gemm_tc_supported(const GemmArgs &g) {
   if (g.epi == EPI_SILU) return false;

@@ -8,15 +8,19 @@
 // not to a 128-row tile. What bounds it is the stream of weights from HBM:
 // each CTA keeps a ring of TMA stages (128 weight rows x 128 bytes of K, and
 // the same K of its tokens) in flight, and K is split over the CTAs of a
-// cluster until every SM has a share of the stream. The CTAs' partial sums
-// (float32, in shared memory as [token][128]) are added through distributed
-// shared memory in rank order, so the result does not depend on timing and no
-// workspace is needed; scales, bias, activation and residual are applied
-// there, on rows of 128 consecutive outputs.
+// cluster until every SM has a share of the stream. A thread of the epilogue
+// holds one weight row (TMEM lane) and its tokens (columns). Without a split it
+// finishes them from registers; with one, groups of 4 tokens are dealt out over
+// the cluster and every CTA sends its float32 sums of a group straight from
+// registers into the owner's shared memory (st.async, counted on the owner's
+// mbarrier; the ring's memory, free once the cluster's products are done), where
+// the same thread adds them in rank order: no workspace, no atomics, and a
+// result that does not depend on timing.
 #include "common.cuh"
 #include "linear.cuh"
 #include "sm100.cuh"
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -29,46 +33,141 @@ constexpr int WROWS = 128;                   // weight rows of a tile
 constexpr int ROW_BYTES = 128;               // bytes of K per stage row (64 bf16 or 128 e4m3)
 constexpr int W_BYTES = WROWS * ROW_BYTES;   // 16 KB
 constexpr int MAX_STAGES = 12;
-constexpr int THREADS = 192;                 // producer, MMA, 4 epilogue warps
+constexpr int THREADS = 192;                 // producer, MMA, 4 epilogue warps (one per quarter of the TMEM lanes)
+constexpr int GROUP = 4;                     // tokens that travel and are finished together
+constexpr int GROUP_BYTES = WROWS * GROUP * 4;
 constexpr int SMEM_MAX = 225 * 1024;
-constexpr int SMEM_HALF = 112 * 1024;        // two CTAs per SM
 
 struct SplitParams {
   int M, N, num_k, split;
-  int mt, stages, nacc, chunk, tmem_cols;    // tokens per tile, ring, accumulators, K steps per accumulator
+  int mt, stages, chunk, tmem_cols;          // tokens per tile, ring, K steps per accumulator
+  int recv;                                  // offset of the receive area; 0: the ring's memory
   uint32_t idesc;
   LinEpilogue e;
   int *watchdog;
 };
 
+// 16 tokens of one weight row n that a thread finishes together: group i + k of
+// 4 tokens is group rank + split (i + k) of the tile. The loads do not look at
+// what they are for until all of them are under way (tokens and columns past
+// the end read the last ones).
 template <bool F8>
-__global__ void __launch_bounds__(THREADS)
+struct Finish {
+  const LinEpilogue &e;
+  int m0, rows, n, N, rank, split;
+  float bias, ws;
+  float res[16], as[16];
+
+  __device__ __forceinline__ int token(int i, int j) const { return (rank + split * (i + j / GROUP)) * GROUP + j % GROUP; }
+
+  __device__ __forceinline__ void fetch(int i) {
+    if (token(i, 0) >= rows) return;
+    if (F8) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) as[j] = e.a_scale[m0 + min(token(i, j), rows - 1)];
+    }
+    if (!e.res) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) res[j] = 0.f;
+      return;
+    }
+    const long long at = (long long)m0 * e.ldr + min(n, N - 1);
+    if (e.res_f32) {
+      const float *p = static_cast<const float *>(e.res) + at;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) res[j] = p[min(token(i, j), rows - 1) * e.ldr];
+    } else {
+      const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(e.res) + at;
+      __nv_bfloat16 h[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) h[j] = p[min(token(i, j), rows - 1) * e.ldr];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) res[j] = __bfloat162float(h[j]);
+    }
+  }
+
+  __device__ __forceinline__ void store(int i, float (&v)[16]) const {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = F8 ? fmaf(v[j], as[j] * ws, bias) : v[j] + bias;
+    lin_act_row(v, e.act);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += res[j];
+    if (n >= N) return;
+    const long long at = (long long)m0 * e.ldo + n;
+    if (e.out_f32) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float *p = static_cast<float *>(e.out) + at + token(i, j) * e.ldo;
+        if (token(i, j) < rows && WAN_DBG_OK(p, 4, e.out, e.out_hi, e.dbg, WAN_DBG_CODE_BASE + 17)) *p = v[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(e.out) + at + token(i, j) * e.ldo;
+        if (token(i, j) < rows && WAN_DBG_OK(p, 2, e.out, e.out_hi, e.dbg, WAN_DBG_CODE_BASE + 17))
+          *p = __float2bfloat16_rn(v[j]);
+      }
+    }
+  }
+};
+
+// T tokens of this lane's weight row from TMEM column `col` on, the accumulators added
+template <int T>
+__device__ __forceinline__ void accumulators(uint32_t tmem, int col, int naccs, int mt, float (&v)[T]) {
+  static_assert(T == 16, "one tcgen05.ld");
+  uint32_t r[T];
+  tmem_ld16(tmem + col, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < T; ++j) v[j] = __uint_as_float(r[j]);
+  for (int a = 1; a < naccs; ++a) {
+    tmem_ld16(tmem + a * mt + col, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < T; ++j) v[j] += __uint_as_float(r[j]);
+  }
+}
+
+template <bool F8>
+__global__ void __launch_bounds__(THREADS, 3)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                     const SplitParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], done;
+  __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], done, arrived;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage_bytes = W_BYTES + p.mt * ROW_BYTES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % p.split;               // cluster rank: the cluster spans x
-  const int n0 = (blockIdx.x / p.split) * WROWS;
+  const int split = p.split, rank = blockIdx.x % split;   // cluster rank: the cluster spans x
+  const int n0 = (blockIdx.x / split) * WROWS;
   const int m0 = blockIdx.y * p.mt;
-  const int kb0 = (int)((long long)p.num_k * rank / p.split);
-  const int nkb = (int)((long long)p.num_k * (rank + 1) / p.split) - kb0;
+  const int kb0 = (int)((long long)p.num_k * rank / split);
+  const int nkb = (int)((long long)p.num_k * (rank + 1) / split) - kb0;
+  const int rows = min(p.mt, p.M - m0);
+  const int groups = (rows + GROUP - 1) / GROUP;
+  const int mine = groups > rank ? (groups - rank - 1) / split + 1 : 0;   // groups rank, rank + split, ...
 
+  auto load = [&](int i, int stage) {
+    const uint32_t fb = smem_u32(&full[stage]), dst = smem_u32(smem + stage * stage_bytes);
+    mbar_arrive_expect_tx(fb, stage_bytes);
+    const int kx = (kb0 + i) * (F8 ? 128 : 64);
+    tma_load_2d(dst, &tmW, kx, n0, fb);
+    tma_load_2d(dst + W_BYTES, &tmA, kx, m0, fb);
+  };
+  const int ahead = min(p.stages, nkb);                 // loads that need no free stage
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     mbar_init(smem_u32(&done), 1);
-    // a wait of an earlier launch gave up: no work, but every barrier below is still passed
-    abort_flag = (p.watchdog && *reinterpret_cast<volatile int *>(p.watchdog)) ? 1 : 0;
+    mbar_init(smem_u32(&arrived), 1);
+    abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmA);
+    for (int i = 0; i < ahead; ++i) load(i, i);
+    // the other CTAs' sums of this CTA's groups
+    mbar_arrive_expect_tx(smem_u32(&arrived), (split - 1) * mine * GROUP_BYTES);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_slot), p.tmem_cols);
@@ -77,162 +176,233 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The cluster's first barrier says that the CTAs' barriers and receive areas
+  // can be written: at once, or when the ring is free.
+  const bool early = p.recv != 0;
+  if (split > 1 && early) cluster_arrive();
   const uint32_t tmem = tmem_slot;
-  const bool skip = abort_flag != 0;
 
-  if (warp == 0 && lane == 0 && !skip) {
+  if (warp == 0) {
     // ------------------------------------------------ TMA producer
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
-    for (; issued < nkb; ++issued) {
-      if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, &abort_flag, p.watchdog, 0x201)) break;
-      const uint32_t fb = smem_u32(&full[stage]);
-      mbar_arrive_expect_tx(fb, stage_bytes);
-      const uint32_t dst = smem_u32(smem + stage * stage_bytes);
-      const int kx = (kb0 + issued) * (F8 ? 128 : 64);
-      tma_load_2d(dst, &tmW, kx, n0, fb);
-      tma_load_2d(dst + W_BYTES, &tmA, kx, m0, fb);
-      if (++stage == p.stages) { stage = 0; phase ^= 1; }
+    if (lane == 0) {
+      int stage = ahead == p.stages ? 0 : ahead, issued = ahead;
+      uint32_t phase = 0;
+      for (; issued < nkb; ++issued) {
+        if (!mbar_wait(smem_u32(&empty[stage]), phase, &abort_flag, p.watchdog, 0x201)) break;
+        load(issued, stage);
+        if (++stage == p.stages) { stage = 0; phase ^= 1; }
+      }
+      // every copy issued has landed before the CTA ends
+      int never = 0;
+      for (int s = 0; s < p.stages; ++s) {
+        const int fills = issued > s ? (issued - 1 - s) / p.stages + 1 : 0;
+        if (fills > 0) mbar_wait(smem_u32(&full[s]), (fills - 1) & 1, &never, p.watchdog, 0x202);
+      }
     }
-    // every copy issued has landed before the stages are reused or the CTA ends
-    int never = 0;
-    for (int s = 0; s < p.stages; ++s) {
-      const int fills = issued > s ? (issued - 1 - s) / p.stages + 1 : 0;
-      if (fills > 0) mbar_wait(smem_u32(&full[s]), (fills - 1) & 1, &never, p.watchdog, 0x202);
+    __syncwarp();
+    if (split > 1) {
+      if (!early) cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
     }
-  } else if (warp == 1 && lane == 0 && !skip) {
+  } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int i = 0, in_chunk = 0, acc = 0; i < nkb; ++i) {
-      if (!mbar_wait(smem_u32(&full[stage]), phase, &abort_flag, p.watchdog, 0x211)) { ok = false; break; }
-      tc_fence_after();
-      const uint32_t base = smem_u32(smem + stage * stage_bytes);
-      const uint64_t aw = desc_kmajor_sw128(base);
-      const uint64_t bt = desc_kmajor_sw128(base + W_BYTES);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {       // 32 bytes of K each: + 2 in 16-byte units
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0, in_chunk = 0, acc = 0; i < nkb; ++i) {
+        if (!mbar_wait(smem_u32(&full[stage]), phase, &abort_flag, p.watchdog, 0x211)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t base = smem_u32(smem + stage * stage_bytes);
+        const uint64_t aw = desc_kmajor_sw128(base);
+        const uint64_t bt = desc_kmajor_sw128(base + W_BYTES);
         const uint32_t d = tmem + acc * p.mt;
-        if (F8) mma_ss_f8(d, aw + 2 * kk, bt + 2 * kk, p.idesc, (in_chunk | kk) != 0);
-        else mma_ss(d, aw + 2 * kk, bt + 2 * kk, p.idesc, (in_chunk | kk) != 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {       // 32 bytes of K each: + 2 in 16-byte units
+          if (F8) mma_ss_f8(d, aw + 2 * kk, bt + 2 * kk, p.idesc, (in_chunk | kk) != 0);
+          else mma_ss(d, aw + 2 * kk, bt + 2 * kk, p.idesc, (in_chunk | kk) != 0);
+        }
+        tc_commit(smem_u32(&empty[stage]));
+        if (++stage == p.stages) { stage = 0; phase ^= 1; }
+        if (++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
       }
-      tc_commit(smem_u32(&empty[stage]));
-      if (++stage == p.stages) { stage = 0; phase ^= 1; }
-      if (++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
+      if (ok) tc_commit(smem_u32(&done));
     }
-    if (ok) tc_commit(smem_u32(&done));
-  } else if (warp >= 2 && !skip) {
-    // ------------------------------------------------ accumulators -> shared memory
-    const bool ok = mbar_wait(smem_u32(&done), 0, &abort_flag, p.watchdog, 0x221);
+    __syncwarp();
+    if (split > 1) {
+      if (!early) cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+    }
+  } else {
+    // ------------------------------------------------ epilogue: weight row n, tokens m0 ..
+    const LinEpilogue &e = p.e;
+    const int q = warp & 3;                  // TMEM lanes this warp may read
+    const int wrow = q * 32 + lane, n = n0 + wrow;
+    const int naccs = (nkb + p.chunk - 1) / p.chunk;
+    const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
+    if (threadIdx.x == 64 && p.watchdog && *reinterpret_cast<volatile int *>(p.watchdog)) abort_flag = 1;   // an earlier launch gave up
+    const float bias = e.bias && n < p.N ? __bfloat162float(e.bias[n]) : 0.f;
+    const float ws = F8 && n < p.N ? e.w_scale[e.w_scale_rows ? n : 0] : 1.f;
+    Finish<F8> f{e, m0, rows, n, p.N, rank, split, bias, ws};
+    f.fetch(0);
+    bool ok = mbar_wait(smem_u32(&done), 0, &abort_flag, p.watchdog, 0x221);
+    ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    if (__all_sync(0xffffffffu, ok)) {
-      // all products are done and their operands read: the ring's memory is free
-      const int q = warp & 3;                // TMEM lanes this warp may read
-      float *part = reinterpret_cast<float *>(smem) + q * 32 + lane;
-      const int naccs = (nkb + p.chunk - 1) / p.chunk;
-      const int cols = min(p.mt, p.M - m0);
-      for (int c = 0; c < cols; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, r);
-        tmem_ld_wait();
+    // sums from rank r of the i-th group of this CTA: recv + (r * most + i) * GROUP_BYTES
+    const int most = (groups + split - 1) / split;
+    uint8_t *recv = smem + p.recv + wrow * 16;
+    if (split > 1) {
+      if (!early) cluster_arrive();
+      cluster_wait();
+      if (ok) {
+        for (int c = 0; c < rows; c += 16) {
+          float v[16];
+          accumulators(taddr, c, naccs, p.mt, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int g = c / GROUP + k, owner = g % split;
+            if (g >= groups) break;
+            const float4 s4 = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            uint8_t *at = recv + (rank * most + g / split) * GROUP_BYTES;
+            if (owner == rank) *reinterpret_cast<float4 *>(at) = s4;
+            else st_async_cluster(mapa_shared(smem_u32(at), owner), s4, mapa_shared(smem_u32(&arrived), owner));
+          }
+        }
+      }
+      cluster_arrive();                      // nothing more leaves this warp
+      if (ok && mine > 0) {
+        ok = mbar_wait_cluster(smem_u32(&arrived), 0, &abort_flag, p.watchdog, 0x222);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+    if (ok) {
+      for (int i = 0; i < mine; i += 4) {
         float v[16];
+        if (split == 1) {
+          accumulators(taddr, i * GROUP, naccs, p.mt, v);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-        for (int a = 1; a < naccs; ++a) {
-          tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + a * p.mt + c, r);
-          tmem_ld_wait();
+          for (int j = 0; j < 16; ++j) v[j] = 0.f;
+          for (int r = 0; r < split; ++r) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+            for (int k = 0; k < 4; ++k) {
+              const float4 x = *reinterpret_cast<const float4 *>(recv + (r * most + min(i + k, mine - 1)) * GROUP_BYTES);
+              v[4 * k] += x.x; v[4 * k + 1] += x.y; v[4 * k + 2] += x.z; v[4 * k + 3] += x.w;
+            }
+          }
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * WROWS] = v[j];
+        f.store(i, v);
+        f.fetch(i + 4);
       }
     }
+    tc_fence_before();
   }
-  __syncwarp();
-  tc_fence_before();
-  if (p.split > 1) cluster_sync_all(); else __syncthreads();
+  if (split > 1) cluster_wait();              // no CTA ends while another still sends to it
+  __syncthreads();
   tc_fence_after();
-
-  // ------------------------------------------------ sum over the cluster, epilogue, stores
-  if (!abort_flag) {
-    const uint32_t part = smem_u32(smem);
-    const int n = n0 + 4 * lane;
-    const int rows = min(p.mt, p.M - m0);
-    LinColumns col;
-    if (n < p.N) col.load(p.e, n, p.N, F8);
-    for (int t = rank + p.split * warp; t < rows; t += p.split * (THREADS / 32)) {
-      const uint32_t off = part + (uint32_t)(t * WROWS + 4 * lane) * 4;
-      float4 v;
-      if (p.split > 1) {
-        v = ld_shared_cluster_f4(mapa_shared(off, 0));
-        for (int r = 1; r < p.split; ++r) {
-          const float4 w = ld_shared_cluster_f4(mapa_shared(off, r));
-          v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-        }
-      } else {
-        v = *reinterpret_cast<const float4 *>(smem + (off - part));
-      }
-      if (n < p.N) lin_store4(p.e, col, m0 + t, n, p.N, v, F8);
-    }
-  }
-  if (p.split > 1) cluster_sync_all();        // the peers have read this CTA's sums
   if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
 }
 
 // ---------------------------------------------------------------- plan
 struct Plan {
-  int mt, split, stages, smem, nacc, chunk, tmem_cols;
+  int mt, split, stages, smem, chunk, tmem_cols, recv;
 };
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
+int recv_bytes(int mt, int split) { return split > 1 ? (mt / GROUP + split - 1) / split * split * GROUP_BYTES : 0; }
+constexpr int SM_SMEM = 228 * 1024, CTA_EXTRA = 1024 + 256;     // of an SM; what a CTA takes besides its ring
+constexpr int SMS = 148;
 
-Plan plan_of(const LinArgs &g) {
-  const int num_k = (g.K + (g.fp8 ? 128 : 64) - 1) / (g.fp8 ? 128 : 64);
-  const int nt = (g.N + WROWS - 1) / WROWS;
-  Plan best = {};
-  double best_cost = 0.0;
+// CTAs of the grid that share an SM. Clusters do not fill a GPC's SMs to the
+// last one: 1 x 5120 x 5120 in 40 clusters of 7 took 20 us with room for two
+// CTAs per SM (280 of 296), 14 us in clusters of 6 or 8.
+long long ctas_per_sm(long long ctas, int split) {
+  const int sms = split > 1 ? SMS * 7 / 8 : SMS;
+  return (ctas + sms - 1) / sms;
+}
+
+long long ctas_of(const LinArgs &g, int mt, int split) {
+  return (long long)((g.N + WROWS - 1) / WROWS) * split * ((g.M + mt - 1) / mt);
+}
+// CTAs that an SM holds at once: all of its own while each keeps three stages
+int resident(const LinArgs &g, int mt, int split) {
+  const int fit = SM_SMEM / (3 * (W_BYTES + mt * ROW_BYTES) + 1024 + CTA_EXTRA);
+  return (int)std::min<long long>(std::min(fit, 3), ctas_per_sm(ctas_of(g, mt, split), split));
+}
+
+Plan make_plan(const LinArgs &g, int num_k, int mt, int split) {
+  const int nkb = (num_k + split - 1) / split;
   // bf16 products are accumulated by the tensor core with a rounding toward
   // zero that grows with the number of steps (relative 1.1e-9 K, measured
   // against 64 bits): harmless under a bf16 output, but a float32 output gets
   // a new accumulator every 64 steps (4096 of K), added in float32
-  const bool chained = !g.fp8 && g.out_f32;
-  const int t0 = (g.M + 255) / 256;
-  for (int t = t0; t <= t0 + 4; ++t) {
-    const int mt = round_up((g.M + t - 1) / t, 16);
-    if (t > t0 && mt < 16) break;
-    const int tiles = (g.M + mt - 1) / mt;
-    for (int split = 1; split <= 8; split *= 2) {
-      if (split > num_k) break;
-      const int nkb = (num_k + split - 1) / split;
-      const int stage = W_BYTES + mt * ROW_BYTES;
-      const int occ = 4 * stage + 1024 <= SMEM_HALF && mt * 512 + 1024 <= SMEM_HALF ? 2 : 1;
-      const int budget = (occ == 2 ? SMEM_HALF : SMEM_MAX) - 1024;
-      int stages = budget / stage;
-      if (stages > MAX_STAGES) stages = MAX_STAGES;
-      int nacc = chained ? (nkb + 63) / 64 : 1;
-      const int most = 512 / occ / mt;
-      if (nacc > most) nacc = most;
-      const int chunk = (nkb + nacc - 1) / nacc;
-      const double kstep = fmax(2.0 * mt, fmax(128.0 + mt, (W_BYTES + mt * 128.0) / 56.0));
-      const double ctas = (double)nt * tiles * split;
-      const double per_sm = ceil(ctas / 148.0);
-      double cost = 4000.0 + per_sm * (nkb * kstep + (per_sm > occ ? 2000.0 : 0.0)) + 6.0 * mt * per_sm + (split > 1 ? 1500.0 : 0.0);
-      const double dram = ((double)g.N + g.M) * g.K * (g.fp8 ? 1 : 2) / 3400.0 + 4000.0 + (split > 1 ? 1500.0 : 0.0);
-      if (dram > cost) cost = dram;
-      if (chained) cost *= 1.0 + 0.5 * (chunk > 64) ;
-      if (best.mt == 0 || cost < best_cost) {
-        best_cost = cost;
-        int cols = 32;
-        while (cols < nacc * mt) cols *= 2;
-        int smem = stages * stage;
-        if (smem < mt * 512) smem = mt * 512;
-        best = Plan{mt, split, stages, smem + 1024, nacc, chunk, cols};
-      }
+  int nacc = !g.fp8 && g.out_f32 ? (nkb + 63) / 64 : 1;
+  nacc = std::min(nacc, 256 / mt);
+  int cols = 32;
+  while (cols < nacc * mt) cols *= 2;
+  const int stage = W_BYTES + mt * ROW_BYTES;
+  // few tokens: a receive area of its own (at most 18 KB) saves a barrier after
+  // the products (14.6 -> 13.4 us at 1 x 5120 x 5120); more would cost stages
+  const int own = split > 1 && mt <= 32 ? recv_bytes(mt, split) : 0;
+  const int per_sm = resident(g, mt, split);
+  int stages = (std::min(SM_SMEM / per_sm - CTA_EXTRA, SMEM_MAX) - 1024 - own) / stage;
+  stages = std::max(2, std::min(std::min(stages, nkb), MAX_STAGES));
+  int smem = (own ? stages * stage + own : std::max(stages * stage, recv_bytes(mt, split))) + 1024;
+  // CTAs of a cluster wait for one another, so none may wait for TMEM that
+  // another cluster holds: a CTA takes at least the share of the SM's shared
+  // memory that it takes of TMEM (456 bytes a column), and what fits, fits
+  smem = std::max(smem, cols * (SM_SMEM / 512) - CTA_EXTRA);
+  return Plan{mt, split, stages, smem, (nkb + nacc - 1) / nacc, cols, own ? stages * stage : 0};
+}
+
+// Time of a plan in SM cycles, to compare plans and kernels by: a start and an
+// end, what an SM takes in for its CTAs, and a new start for every further wave.
+// Measured: an SM takes in 28 bytes a cycle from HBM (22 with one CTA) and 55
+// from L2 (an operand comes from HBM for the first tile that reads it), and the
+// card 3400 from HBM.
+double split_cost(const LinArgs &g, int num_k, int mt, int split) {
+  const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + mt - 1) / mt;
+  const double per_sm = (double)ctas_per_sm(ctas_of(g, mt, split), split);
+  const int nkb = (num_k + split - 1) / split;
+  const double hbm = per_sm > 1.0 ? 28.0 : 22.0;
+  auto ingest = [&](double bytes, double readers) { return bytes * (1.0 / hbm / readers + (1.0 - 1.0 / readers) / 55.0); };
+  const double step = ingest(W_BYTES, ntm) + ingest((double)std::min(mt, g.M) * ROW_BYTES, ntn);
+  const double dram = ((double)g.M + g.N) * g.K * (g.fp8 ? 1 : 2) / 3400.0;
+  return 9500.0 + 10.0 * mt * per_sm + (split > 1 ? 100.0 * split : 0.0) +
+         4000.0 * (ceil(per_sm / resident(g, mt, split)) - 1.0) + std::max(per_sm * nkb * step, dram);
+}
+// The same of the pair kernel: 256 x 256 tiles in rounds of 74 pairs, 600
+// cycles a step of K or the tile's epilogue (9000 cycles; 20000 where the rows
+// of out or residual are out of the TMA unit's reach), the last one in the open.
+double pair_cost(const LinArgs &g, int num_k) {
+  const double tiles = ceil(g.M / 256.0) * ceil(g.N / 256.0);
+  const LinEpilogue e = lin_epilogue(g);
+  const double epi = e.vec_out && e.vec_res ? 9000.0 : 20000.0;
+  return 8000.0 + epi + ceil(tiles / 74.0) * std::max(num_k * 600.0, epi);
+}
+
+// False: the pair kernel.
+bool plan_of(const LinArgs &g, Plan &plan) {
+  const int num_k = (g.K + (g.fp8 ? 128 : 64) - 1) / (g.fp8 ? 128 : 64);
+  int best_mt = 0, best_split = 0;
+  double best = 0.0;
+  for (int want = 16; want <= 128; want += 16) {
+    if (want > 16 && want - 16 >= g.M) break;
+    const int tiles = (g.M + want - 1) / want, mt = round_up((g.M + tiles - 1) / tiles, 16);
+    for (int split = 1; split <= std::min(8, num_k); ++split) {
+      const double c = split_cost(g, num_k, mt, split);
+      if (!best_mt || c < best) { best = c; best_mt = mt; best_split = split; }
     }
   }
-  return best;
+  // the pair kernel keeps one accumulator per tile: not for float32 outputs of
+  // bf16 sums longer than 4096 (make_plan)
+  const bool chained = !g.fp8 && g.out_f32 && g.K > 4096;
+  const bool fits = (g.M + best_mt - 1) / best_mt <= 65535;
+  if (!chained && (!fits || pair_cost(g, num_k) < best)) return false;
+  plan = make_plan(g, num_k, best_mt, best_split);
+  return true;
 }
 
 template <bool F8>
@@ -258,7 +428,7 @@ int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
   }
   SplitParams p = {};
   p.M = g.M; p.N = g.N; p.num_k = (g.K + (F8 ? 128 : 64) - 1) / (F8 ? 128 : 64); p.split = pl.split;
-  p.mt = pl.mt; p.stages = pl.stages; p.nacc = pl.nacc; p.chunk = pl.chunk; p.tmem_cols = pl.tmem_cols;
+  p.mt = pl.mt; p.stages = pl.stages; p.chunk = pl.chunk; p.recv = pl.recv; p.tmem_cols = pl.tmem_cols;
   p.idesc = F8 ? idesc_e4m3(WROWS, pl.mt) : idesc_bf16(WROWS, pl.mt, 0);
   p.e = lin_epilogue(g);
   p.watchdog = watchdog_ptr();
@@ -278,7 +448,8 @@ int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
 }  // namespace
 
 int launch_linear(const LinArgs &g, cudaStream_t s) {
-  const Plan pl = plan_of(g);
+  Plan pl;
+  if (!plan_of(g, pl)) return gemm_tc_linear(g, s);
   if ((g.M + pl.mt - 1) / pl.mt > 65535) return set_error(WAN_EINVAL, "linear: M=%d too large", g.M);
   return g.fp8 ? launch<true>(g, pl, s) : launch<false>(g, pl, s);
 }

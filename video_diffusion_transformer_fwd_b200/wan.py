@@ -293,9 +293,15 @@ def profile_read():
 
 
 # ---------------------------------------------------------------- torch helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -310,10 +316,10 @@ def _stream(stream=None):
 
 
 def dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
+    torch, dt = _torch(), t.dtype
+    if dt == torch.bfloat16:
         return WAN_BF16
-    if t.dtype == torch.float32:
+    if dt == torch.float32:
         return WAN_F32
     raise TypeError(f"unsupported dtype {t.dtype}")
 
@@ -366,43 +372,52 @@ def linear_fp8(a, a_scale, w, w_scale, bias=None, out=None, stream=None):
 ACTIVATIONS = {"none": WAN_ACT_NONE, "gelu_tanh": WAN_ACT_GELU_TANH, "silu": WAN_ACT_SILU, "relu": WAN_ACT_RELU}
 
 
-def _elem_code(t) -> int:
-    """dtype_code, and WAN_FP8 for e4m3 codes (uint8 or float8_e4m3fn)."""
-    torch = _torch()
-    if t.dtype == torch.uint8 or t.dtype == torch.float8_e4m3fn:
-        return WAN_FP8
-    return dtype_code(t)
+class _Types:
+    """Type codes of torch dtypes (with torch imported on first use)."""
+    codes = None
+
+    @classmethod
+    def get(cls):
+        if cls.codes is None:
+            torch = _torch()
+            cls.codes = {torch.float32: WAN_F32, torch.bfloat16: WAN_BF16, torch.uint8: WAN_FP8,
+                         torch.float8_e4m3fn: WAN_FP8}
+        return cls.codes
 
 
-def _rows(t, name):
-    """t as a matrix of its last axis (a view) and its row stride in elements."""
-    m = t if t.dim() == 2 else t.view(-1, t.shape[-1])
-    rows, cols = m.shape
-    if cols > 1 and m.stride(1) != 1:
+# Small calls are bound by the host: the helpers of wan_rmsnorm and wan_linear
+# look at each tensor once and make one library call.
+def _matrix(t, name, shape, rows, dev):
+    """Address and row stride (in elements) of t, which must have this shape, as
+    a matrix of its last axis (rows: the product of the other axes)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if len(shape) != 2:
+        t = t.view(rows, shape[-1])
+    ld, unit = t.stride()
+    if unit != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    ld = m.stride(0) if rows > 1 else cols
-    return m, ld
+    return t.data_ptr(), (ld if rows > 1 else shape[-1])
 
 
-def _one_device(**tensors):
-    """Index of the CUDA device that holds every tensor given."""
-    idx = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{name} is not on a CUDA device")
-        if idx is None:
-            idx = d
-        elif d != idx:
-            raise ValueError(f"{name} is on cuda:{d}, the other tensors on cuda:{idx}")
-    return idx
-
-
-def _vector(t, name, n, dtype):
+def _vector(t, name, n, dtype, dev):
+    """Address of a contiguous vector of n elements."""
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    """Handle of the stream, by default of the current one of device dev."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _empty_on(stream, shape, dtype, device):
@@ -424,46 +439,48 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
     that are not given are allocated. Rows may be strided (2-D tensors).
     Returns (y, row_scale, h): row_scale is None unless y holds codes, h is x
     itself without a residual and has the residual's type with one."""
-    torch = _torch()
-    dev = _one_device(x=x, gain=gain, residual=residual, out=out, row_scale=row_scale, h_out=h_out)
+    torch, codes = _torch(), _Types.codes or _Types.get()
+    dev, shape = x.get_device(), x.shape
+    if dev < 0:
+        raise ValueError("x is not on a CUDA device")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return rmsnorm(x, gain, residual, eps, out_dtype, out, row_scale, h_out, stream)
-    if x.dim() == 0 or x.shape[-1] == 0:
+    if not shape or not shape[-1]:
         raise ValueError("x needs a last axis to normalise")
-    code = (_elem_code(out) if out is not None else dtype_code(x)) if out_dtype is None else DTYPE_CODES[out_dtype]
+    D = shape[-1]
+    rows = x.numel() // D
+    xc = dtype_code(x)
     if out is None:
-        out = _empty_on(stream, x.shape, {WAN_FP8: torch.uint8, WAN_BF16: torch.bfloat16, WAN_F32: torch.float32}[code],
-                        x.device)
-    elif _elem_code(out) != code:
-        raise ValueError(f"out has type {out.dtype}, not {out_dtype}")
-    xm, ldx = _rows(x, "x")
-    ym, ldy = _rows(out, "out")
-    rows, D = xm.shape
-    if out.shape != x.shape or (residual is not None and residual.shape != x.shape) or \
-            (h_out is not None and h_out.shape != x.shape):
-        raise ValueError("x, residual, out and h_out must have one shape")
-    if gain is not None:
-        _vector(gain, "gain", D, torch.float32)
+        code = xc if out_dtype is None else DTYPE_CODES[out_dtype]
+        out = _empty_on(stream, shape, {WAN_FP8: torch.uint8, WAN_BF16: torch.bfloat16, WAN_F32: torch.float32}[code], x.device)
+    else:
+        code = codes.get(out.dtype)
+        if code is None or (out_dtype is not None and DTYPE_CODES[out_dtype] != code):
+            raise ValueError(f"out has type {out.dtype}")
+    xp, ldx = _matrix(x, "x", shape, rows, dev)
+    yp, ldy = _matrix(out, "out", shape, rows, dev)
+    gp = None if gain is None else _vector(gain, "gain", D, torch.float32, dev)
+    sp = None
     if code == WAN_FP8:
         if row_scale is None:
-            row_scale = _empty_on(stream, x.shape[:-1], torch.float32, x.device)
-        _vector(row_scale, "row_scale", rows, torch.float32)
+            row_scale = _empty_on(stream, shape[:-1], torch.float32, x.device)
+        sp = _vector(row_scale, "row_scale", rows, torch.float32, dev)
     elif row_scale is not None:
         raise ValueError("row_scale goes with e4m3 codes")
-    rcode, rm, ldr, hm, ldh = WAN_F32, None, 0, None, 0
+    rc, rp, ldr, hp, ldh = WAN_F32, None, 0, None, 0
     if residual is not None:
-        rcode = dtype_code(residual)
-        rm, ldr = _rows(residual, "residual")
+        rc = dtype_code(residual)
+        rp, ldr = _matrix(residual, "residual", shape, rows, dev)
         if h_out is None:
-            h_out = _empty_on(stream, x.shape, residual.dtype, x.device)
+            h_out = _empty_on(stream, shape, residual.dtype, x.device)
         elif h_out.dtype != residual.dtype:
             raise ValueError("h_out has the residual's type")
-        hm, ldh = _rows(h_out, "h_out")
+        hp, ldh = _matrix(h_out, "h_out", shape, rows, dev)
     elif h_out is not None:
         raise ValueError("h_out needs a residual")
-    check(wan_rmsnorm(rows, D, xm.data_ptr(), dtype_code(x), ldx, _ptr(rm), rcode, ldr, _ptr(gain), eps, _ptr(hm), ldh,
-                      ym.data_ptr(), code, ldy, _ptr(row_scale), _stream(stream)))
+    check(load().wan_rmsnorm(rows, D, xp, xc, ldx, rp, rc, ldr, gp, eps, hp, ldh, yp, code, ldy, sp,
+                             _raw_stream(stream, dev)))
     return out, row_scale, (x if residual is None else h_out)
 
 
@@ -479,49 +496,48 @@ def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_sc
     ``out_dtype`` is "bf16" or "f32" (by default the type of ``out``, of the
     residual, or bf16). Rows may be strided (2-D tensors); those of a and w
     start on 16-byte boundaries. Returns out [..., N]."""
-    torch = _torch()
-    dev = _one_device(a=a, w=w, bias=bias, residual=residual, a_scale=a_scale, w_scale=w_scale, out=out)
+    torch, codes = _torch(), _Types.codes or _Types.get()
+    dev = a.get_device()
+    if dev < 0:
+        raise ValueError("a is not on a CUDA device")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return linear(a, w, bias, activation, residual, a_scale, w_scale, out, out_dtype, stream)
-    code = _elem_code(a)
-    if _elem_code(w) != code:
+    code = codes.get(a.dtype)
+    if code is None or codes.get(w.dtype) != code:
         raise ValueError(f"a has type {a.dtype}, w {w.dtype}")
-    if w.dim() != 2 or a.dim() == 0 or a.shape[-1] != w.shape[1]:
-        raise ValueError(f"a {tuple(a.shape)} does not fit w {tuple(w.shape)}")
-    N, K = w.shape
-    shape = a.shape[:-1] + (N,)
+    ash, wsh = a.shape, w.shape
+    if len(wsh) != 2 or not ash or ash[-1] != wsh[1]:
+        raise ValueError(f"a {tuple(ash)} does not fit w {tuple(wsh)}")
+    N, K = wsh
+    shape = ash[:-1] + (N,)
     if out is None:
         dt = {"bf16": torch.bfloat16, "f32": torch.float32, None: torch.bfloat16 if residual is None else residual.dtype}[out_dtype]
         out = _empty_on(stream, shape, dt, a.device)
     elif out_dtype is not None and dtype_code(out) != DTYPE_CODES[out_dtype]:
         raise ValueError(f"out has type {out.dtype}, not {out_dtype}")
-    if out.shape != shape or (residual is not None and residual.shape != shape):
-        raise ValueError(f"out and residual must have shape {tuple(shape)}")
-    if N == 0:
+    if not N:
         return out
-    am, lda = _rows(a, "a")
-    wm, ldw = _rows(w, "w")
-    om, ldo = _rows(out, "out")
-    M = am.shape[0]
-    rows = 0
+    M = a.numel() // K if K else out.numel() // N
+    ap, lda = _matrix(a, "a", ash, M, dev)
+    wp, ldw = _matrix(w, "w", wsh, N, dev)
+    op, ldo = _matrix(out, "out", shape, M, dev)
+    per_row, asp, wsp = 0, None, None
     if code == WAN_FP8:
         if a_scale is None or w_scale is None:
             raise ValueError("e4m3 operands need a_scale and w_scale")
-        rows = 1 if w_scale.numel() == N and N > 1 else 0
-        _vector(a_scale, "a_scale", M, torch.float32)
-        _vector(w_scale, "w_scale", N if rows else 1, torch.float32)
+        per_row = 1 if N > 1 and w_scale.numel() == N else 0
+        asp = _vector(a_scale, "a_scale", M, torch.float32, dev)
+        wsp = _vector(w_scale, "w_scale", N if per_row else 1, torch.float32, dev)
     elif a_scale is not None or w_scale is not None:
         raise ValueError("bf16 operands have no scales")
-    if bias is not None:
-        _vector(bias, "bias", N, torch.bfloat16)
-    rcode, rm, ldr = WAN_F32, None, 0
+    bp = None if bias is None else _vector(bias, "bias", N, torch.bfloat16, dev)
+    rc, rp, ldr = WAN_F32, None, 0
     if residual is not None:
-        rcode = dtype_code(residual)
-        rm, ldr = _rows(residual, "residual")
-    check(wan_linear(M, N, K, code, am.data_ptr(), lda, _ptr(a_scale), wm.data_ptr(), ldw, _ptr(w_scale), rows,
-                     _ptr(bias), ACTIVATIONS[activation], _ptr(rm), rcode, ldr, om.data_ptr(), dtype_code(out), ldo,
-                     _stream(stream)))
+        rc = dtype_code(residual)
+        rp, ldr = _matrix(residual, "residual", shape, M, dev)
+    check(load().wan_linear(M, N, K, code, ap, lda, asp, wp, ldw, wsp, per_row, bp, ACTIVATIONS[activation], rp, rc, ldr,
+                            op, dtype_code(out), ldo, _raw_stream(stream, dev)))
     return out
 
 
