@@ -402,13 +402,19 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
  * Products are accumulated in float32 on the tensor cores, everything after
  * them is float32, and the result is rounded once. A stride is ignored where
  * its matrix has one row. No workspace. M or N = 0 is an empty call.
- * The first call on a device must come before any stream capture.
+ * The first call on a device must come before any stream capture. The struct
+ * is read during the call.
  * Errors: WAN_EINVAL (sizes, NULLs, strides below the width, overlaps),
  * WAN_EALIGN (pointers, lda, ldw), WAN_EUNSUPPORTED (dtypes, activation). */
-int wan_linear(int M, int N, int K, int dtype, const void *a, long long lda, const float *a_scale,
-               const void *w, long long ldw, const float *w_scale, int w_scale_rows,
-               const void *bias, int activation, const void *residual, int res_dtype, long long ldr,
-               void *out, int out_dtype, long long ldo, wan_stream_t stream);
+typedef struct {
+  const void *a, *w;
+  const float *a_scale, *w_scale;
+  const void *bias, *residual;
+  void *out;
+  int64_t lda, ldw, ldr, ldo;
+  int M, N, K, dtype, w_scale_rows, activation, res_dtype, out_dtype;
+} wan_linear_args;
+int wan_linear(const wan_linear_args *args, wan_stream_t stream);
 
 /* wan_rmsnorm -- RMS norm of every row with the residual's addition, and an
  * output in e4m3 for the FP8 product that follows it:
@@ -428,14 +434,22 @@ int wan_linear(int M, int N, int K, int dtype, const void *a, long long lda, con
  *             scale 0; a row with a NaN or an infinity: scale and codes NaN).
  *   An output may be exactly an input matrix (same address, element size and
  *   stride: h_out = residual, y = x, ...), and overlaps nothing else. What
- *   lies between the rows of an output stays.
+ *   lies between the rows of an output stays; what lies between the rows of
+ *   an input may be read and has no effect.
  * h, the sum of squares, y and the scale are float32; the norm takes h before
  * it is rounded into h_out. rows = 0 is an empty call.
  * Errors: WAN_EINVAL (sizes, NULLs, strides below D, overlaps), WAN_EALIGN,
  * WAN_EUNSUPPORTED (D > 16384, dtypes). */
-int wan_rmsnorm(int rows, int D, const void *x, int x_dtype, long long ldx, const void *residual,
-                int res_dtype, long long ldr, const float *gain, float eps, void *h_out, long long ldh,
-                void *y, int y_dtype, long long ldy, float *row_scale, wan_stream_t stream);
+typedef struct {
+  const void *x, *residual;
+  const float *gain;
+  void *h_out, *y;
+  float *row_scale;
+  int64_t ldx, ldr, ldh, ldy;
+  int rows, D, x_dtype, res_dtype, y_dtype;
+  float eps;
+} wan_rmsnorm_args;
+int wan_rmsnorm(const wan_rmsnorm_args *args, wan_stream_t stream);
 
 /* UniPC multistep sampler for the latent ("Wan2.2 I2V inference trace",
  * section 4 "DIT": the latent update "UniPC: x_noise <- step(v, t, x_noise)";

@@ -64,7 +64,7 @@ def check(x, r, g, out, y, scale, h, eps=EPS):
 # one thread to several per row, one warp, one CTA of every register depth; the
 # same for widths that are not multiples of 8
 WIDTHS = [8, 16, 64, 72, 128, 136, 256, 264, 512, 520, 1536, 2048, 2056, 4096, 5120, 8192, 8200, 13824, 16384]
-RAGGED = [1, 3, 31, 33, 127, 129, 1037, 2047, 2049, 7031, 16383]
+RAGGED = [1, 3, 7, 9, 31, 33, 57, 58, 127, 129, 500, 507, 1037, 2047, 2049, 7031, 16366, 16370, 16371, 16383]
 
 
 @pytest.mark.parametrize("D", WIDTHS + RAGGED)
@@ -87,7 +87,7 @@ def test_types(x, r, out, rows, D):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 3, 7, 8, 9, 16, 17, 1000])
-@pytest.mark.parametrize("D", [64, 128, 200, 1000])
+@pytest.mark.parametrize("D", [64, 71, 128, 200, 250, 1000, 1037])
 def test_row_counts_and_guards(rows, D):
     """Rows that do not fill the last CTA; bytes around every output stay."""
     x, r, g = make(rows, D)
@@ -118,23 +118,27 @@ def test_no_gain_no_stored_sum_and_leading_axes():
     assert y.shape == h.shape == (2, 3, 256)
     check(x, r, None, "f32", y.view(6, 256), None, h.view(6, 256))
     y2 = torch.empty_like(y)
-    st = torch.cuda.current_stream().cuda_stream
-    assert wan.wan_rmsnorm(6, 256, x.data_ptr(), wan.WAN_BF16, 256, r.data_ptr(), wan.WAN_F32, 256, None, EPS, None, 0,
-                           y2.data_ptr(), wan.WAN_F32, 256, None, st) == wan.WAN_OK
+    args = wan.wan_rmsnorm_args(x=x.data_ptr(), residual=r.data_ptr(), y=y2.data_ptr(), ldx=256, ldr=256, ldy=256, rows=6,
+                                D=256, x_dtype=wan.WAN_BF16, res_dtype=wan.WAN_F32, y_dtype=wan.WAN_F32, eps=EPS)
+    assert wan.wan_rmsnorm(args, torch.cuda.current_stream().cuda_stream) == wan.WAN_OK
     torch.cuda.synchronize()
     assert torch.equal(y, y2)
 
 
-@pytest.mark.parametrize("D,pad", [(256, 8), (256, 24), (250, 6), (1000, 5)])
-def test_strided_rows_leave_the_gaps(D, pad):
+# pads of x, residual, y, h_out: strides that agree modulo 8 (aligned rows, and
+# shifted ones with widths that end anywhere), and strides that do not
+@pytest.mark.parametrize("D,pads", [(256, (8, 8, 8, 8)), (256, (24, 8, 0, 16)), (250, (6, 6, 6, 6)), (250, (1, 9, 1, 17)),
+                                    (1003, (2, 2, 10, 2)), (1000, (5, 5, 5, 5)), (1000, (5, 6, 7, 9)), (256, (1, 2, 3, 4)),
+                                    (5, (3, 4, 0, 1)), (3001, (0, 1, 2, 0)), (9000, (1, 0, 0, 0))])
+def test_strided_rows_leave_the_gaps(D, pads):
     """Rows further apart than D: NaN between input rows is not read, and what
     lies between output rows stays."""
     rows = 9
     x, r, g = make(rows, D)
-    big = [torch.full((rows, D + pad), float("nan"), device="cuda", dtype=t.dtype) for t in (x, r)]
+    big = [torch.full((rows, D + p), float("nan"), device="cuda", dtype=t.dtype) for t, p in zip((x, r), pads)]
     for b, t in zip(big, (x, r)):
         b[:, :D] = t
-    outs = [torch.full((rows, D + pad), 7, device="cuda", dtype=dt) for dt in (torch.float32, torch.float32)]
+    outs = [torch.full((rows, D + p), 7, device="cuda", dtype=torch.float32) for p in pads[2:]]
     y, _, h = wan.rmsnorm(big[0][:, :D], g, residual=big[1][:, :D], out=outs[0][:, :D], h_out=outs[1][:, :D])
     check(x, r, g, "f32", y, None, h)
     assert all(bool((o[:, D:] == 7).all()) for o in outs)
@@ -143,7 +147,7 @@ def test_strided_rows_leave_the_gaps(D, pad):
 
 
 def test_in_place():
-    for D in (512, 1037):
+    for D in (512, 1037, 3163):
         x, r, g = make(11, D, r="bf16")
         y, _, h = wan.rmsnorm(x, g, residual=r)
         x2, r2 = x.clone(), r.clone()

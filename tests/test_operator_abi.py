@@ -1,5 +1,7 @@
 """wan_rmsnorm and wan_linear refuse bad calls on the host, before any launch
 (no GPU is touched: every call here returns before a CUDA call is made)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -20,7 +22,8 @@ def norm(**kw):
              gain=3 * MB, eps=1e-6, h_out=4 * MB, ldh=64, y=5 * MB, y_dtype=wan.WAN_FP8, ldy=64, row_scale=6 * MB,
              stream=None)
     a.update(kw)
-    return wan.wan_rmsnorm(*a.values())
+    stream = a.pop("stream")
+    return wan.wan_rmsnorm(wan.wan_rmsnorm_args(**a), stream)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -49,7 +52,8 @@ def lin(**kw):
              w_scale_rows=1, bias=5 * MB, activation=wan.WAN_ACT_SILU, residual=6 * MB, res_dtype=wan.WAN_F32, ldr=48,
              out=7 * MB, out_dtype=wan.WAN_F32, ldo=48, stream=None)
     a.update(kw)
-    return wan.wan_linear(*a.values())
+    stream = a.pop("stream")
+    return wan.wan_linear(wan.wan_linear_args(**a), stream)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -71,6 +75,19 @@ def lin(**kw):
 def test_linear_refusals(kw, code):
     assert lin(**kw) == code
     assert code == OK or wan.last_error()
+
+
+def test_null_arguments():
+    assert wan.wan_rmsnorm(None, None) == EINVAL and wan.wan_linear(None, None) == EINVAL
+
+
+def test_packed_layouts_are_the_structs():
+    """The helpers' packed arguments have the layout of the ctypes structures."""
+    for fmt, cls in ((wan._LINEAR_ARGS, wan.wan_linear_args), (wan._RMSNORM_ARGS, wan.wan_rmsnorm_args)):
+        assert fmt.size == ctypes.sizeof(cls)
+        values = list(range(1, len(cls._fields_) + 1))
+        got = cls.from_buffer_copy(fmt.pack(*values))
+        assert [getattr(got, n) for n, _ in cls._fields_] == values
 
 
 def test_python_helpers_refuse_host_tensors():

@@ -732,10 +732,10 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
   return WAN_PROF(WAN_K_GEMM_TC, s, gemm_tc(g, s));
 }
 
-int wan_rmsnorm(int rows, int D, const void *x, int x_dtype, long long ldx, const void *residual, int res_dtype,
-                long long ldr, const float *gain, float eps, void *h_out, long long ldh, void *y, int y_dtype,
-                long long ldy, float *row_scale, wan_stream_t stream) {
+int wan_rmsnorm(const wan_rmsnorm_args *args, wan_stream_t stream) {
   g_msg[0] = 0;
+  if (!args) return set_error(WAN_EINVAL, "rmsnorm: args is NULL");
+  const auto &[x, residual, gain, h_out, y, row_scale, ldx, ldr, ldh, ldy, rows, D, x_dtype, res_dtype, y_dtype, eps] = *args;
   if (rows < 0 || D < 1) return set_error(WAN_EINVAL, "rmsnorm: rows %d, D %d", rows, D);
   if (D > RMS_MAX_D) return set_error(WAN_EUNSUPPORTED, "rmsnorm: D %d > %d", D, RMS_MAX_D);
   if (!(eps >= 0.f)) return set_error(WAN_EINVAL, "rmsnorm: eps must be >= 0");
@@ -755,11 +755,12 @@ int wan_rmsnorm(int rows, int D, const void *x, int x_dtype, long long ldx, cons
                                                      ldh, y, y_dtype, ldy, row_scale, s));
 }
 
-int wan_linear(int M, int N, int K, int dtype, const void *a, long long lda, const float *a_scale, const void *w,
-               long long ldw, const float *w_scale, int w_scale_rows, const void *bias, int activation,
-               const void *residual, int res_dtype, long long ldr, void *out, int out_dtype, long long ldo,
-               wan_stream_t stream) {
+int wan_linear(const wan_linear_args *args, wan_stream_t stream) {
   g_msg[0] = 0;
+  if (!args) return set_error(WAN_EINVAL, "linear: args is NULL");
+  const auto &[a, w, a_scale, w_scale, bias, residual, out, lda_, ldw_, ldr_, ldo_, M, N, K, dtype, w_scale_rows,
+               activation, res_dtype, out_dtype] = *args;
+  long long lda = lda_, ldw = ldw_, ldr = ldr_, ldo = ldo_;
   if (M < 0 || N < 0 || K < 1) return set_error(WAN_EINVAL, "linear: M %d N %d K %d", M, N, K);
   if (dtype != WAN_BF16 && dtype != WAN_FP8) return set_error(WAN_EUNSUPPORTED, "linear: operand dtype %d", dtype);
   if (!is_float_dtype(out_dtype) || (residual && !is_float_dtype(res_dtype)))

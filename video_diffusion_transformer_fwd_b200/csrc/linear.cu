@@ -448,10 +448,24 @@ int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
 }  // namespace
 
 int launch_linear(const LinArgs &g, cudaStream_t s) {
-  Plan pl;
-  if (!plan_of(g, pl)) return gemm_tc_linear(g, s);
-  if ((g.M + pl.mt - 1) / pl.mt > 65535) return set_error(WAN_EINVAL, "linear: M=%d too large", g.M);
-  return g.fp8 ? launch<true>(g, pl, s) : launch<false>(g, pl, s);
+  // the choice costs a few microseconds of the host: the last ones are kept, by sizes and types
+  struct Known {
+    int M, N, K, kind;
+    bool split;
+    Plan plan;
+  };
+  thread_local Known known[32] = {};
+  const LinEpilogue e = lin_epilogue(g);
+  const int kind = 1 | (g.fp8 ? 2 : 0) | (g.out_f32 ? 4 : 0) | (e.vec_out && e.vec_res ? 8 : 0);
+  const unsigned h = ((unsigned)g.M * 2654435761u ^ (unsigned)g.N * 40503u ^ (unsigned)g.K * 65599u ^ (unsigned)kind) >> 3;
+  Known &k = known[h % 32];
+  if (k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
+    k = Known{g.M, g.N, g.K, kind, false, Plan{}};
+    k.split = plan_of(g, k.plan);
+  }
+  if (!k.split) return gemm_tc_linear(g, s);
+  if ((g.M + k.plan.mt - 1) / k.plan.mt > 65535) return set_error(WAN_EINVAL, "linear: M=%d too large", g.M);
+  return g.fp8 ? launch<true>(g, k.plan, s) : launch<false>(g, k.plan, s);
 }
 
 }  // namespace wan

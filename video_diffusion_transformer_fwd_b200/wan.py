@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libwan.so")
@@ -70,7 +71,25 @@ class wan_model_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in MODEL_WEIGHT_FIELDS]
 
 
-_c_int, _vp, _sz, _ll = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong
+class wan_linear_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("a", "w", "a_scale", "w_scale", "bias", "residual", "out")] +
+                [(n, ctypes.c_int64) for n in ("lda", "ldw", "ldr", "ldo")] +
+                [(n, ctypes.c_int) for n in ("M", "N", "K", "dtype", "w_scale_rows", "activation", "res_dtype",
+                                             "out_dtype")])
+
+
+class wan_rmsnorm_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "gain", "h_out", "y", "row_scale")] +
+                [(n, ctypes.c_int64) for n in ("ldx", "ldr", "ldh", "ldy")] +
+                [(n, ctypes.c_int) for n in ("rows", "D", "x_dtype", "res_dtype", "y_dtype")] +
+                [("eps", ctypes.c_float)])
+
+
+# the same layouts for struct.pack: a small call is bound by its host work, and
+# one packed argument costs a quarter of twenty converted ones
+_LINEAR_ARGS, _RMSNORM_ARGS = struct.Struct("@7P4q8i"), struct.Struct("@6P4q5if")
+
+_c_int, _vp, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 
 _SIGS = {
     "wan_last_error": (ctypes.c_char_p, []),
@@ -100,10 +119,8 @@ _SIGS = {
     "wan_model_workspace_bytes": (_sz, [ctypes.POINTER(wan_model_dims), _c_int]),
     "wan_quantize_fp8": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "wan_linear_fp8": (_c_int, [_c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
-    "wan_linear": (_c_int, [_c_int, _c_int, _c_int, _c_int, _vp, _ll, _vp, _vp, _ll, _vp, _c_int, _vp, _c_int, _vp,
-                            _c_int, _ll, _vp, _c_int, _ll, _vp]),
-    "wan_rmsnorm": (_c_int, [_c_int, _c_int, _vp, _c_int, _ll, _vp, _c_int, _ll, _vp, ctypes.c_float, _vp, _ll, _vp,
-                             _c_int, _ll, _vp, _vp]),
+    "wan_linear": (_c_int, [_vp, _vp]),
+    "wan_rmsnorm": (_c_int, [_vp, _vp]),
     "wan_attention_8bit_workspace_bytes": (_sz, [_c_int, _c_int, _c_int, _c_int]),
     "wan_unipc_coefficients": (_c_int, [ctypes.POINTER(ctypes.c_double), _c_int, _c_int, _c_int, _c_int,
                                         ctypes.POINTER(ctypes.c_double)]),
@@ -230,16 +247,14 @@ def wan_linear_fp8(M, N, K, a, a_scale, w, w_scale, bias, out, stream):
     return load().wan_linear_fp8(M, N, K, a, a_scale, w, w_scale, bias, out, stream)
 
 
-def wan_linear(M, N, K, dtype, a, lda, a_scale, w, ldw, w_scale, w_scale_rows, bias, activation, residual, res_dtype,
-               ldr, out, out_dtype, ldo, stream):
-    return load().wan_linear(M, N, K, dtype, a, lda, a_scale, w, ldw, w_scale, w_scale_rows, bias, activation,
-                             residual, res_dtype, ldr, out, out_dtype, ldo, stream)
+def wan_linear(args, stream):
+    """args: a wan_linear_args, or None."""
+    return load().wan_linear(None if args is None else ctypes.addressof(args), stream)
 
 
-def wan_rmsnorm(rows, D, x, x_dtype, ldx, residual, res_dtype, ldr, gain, eps, h_out, ldh, y, y_dtype, ldy, row_scale,
-                stream):
-    return load().wan_rmsnorm(rows, D, x, x_dtype, ldx, residual, res_dtype, ldr, gain, eps, h_out, ldh, y, y_dtype,
-                              ldy, row_scale, stream)
+def wan_rmsnorm(args, stream):
+    """args: a wan_rmsnorm_args, or None."""
+    return load().wan_rmsnorm(None if args is None else ctypes.addressof(args), stream)
 
 
 def wan_attention_8bit_workspace_bytes(B, heads, Lq, Lk):
@@ -443,7 +458,7 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
     dev, shape = x.get_device(), x.shape
     if dev < 0:
         raise ValueError("x is not on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return rmsnorm(x, gain, residual, eps, out_dtype, out, row_scale, h_out, stream)
     if not shape or not shape[-1]:
@@ -460,15 +475,15 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
             raise ValueError(f"out has type {out.dtype}")
     xp, ldx = _matrix(x, "x", shape, rows, dev)
     yp, ldy = _matrix(out, "out", shape, rows, dev)
-    gp = None if gain is None else _vector(gain, "gain", D, torch.float32, dev)
-    sp = None
+    gp = 0 if gain is None else _vector(gain, "gain", D, torch.float32, dev)
+    sp = 0
     if code == WAN_FP8:
         if row_scale is None:
             row_scale = _empty_on(stream, shape[:-1], torch.float32, x.device)
         sp = _vector(row_scale, "row_scale", rows, torch.float32, dev)
     elif row_scale is not None:
         raise ValueError("row_scale goes with e4m3 codes")
-    rc, rp, ldr, hp, ldh = WAN_F32, None, 0, None, 0
+    rc, rp, ldr, hp, ldh = WAN_F32, 0, 0, 0, 0
     if residual is not None:
         rc = dtype_code(residual)
         rp, ldr = _matrix(residual, "residual", shape, rows, dev)
@@ -479,7 +494,7 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
         hp, ldh = _matrix(h_out, "h_out", shape, rows, dev)
     elif h_out is not None:
         raise ValueError("h_out needs a residual")
-    check(load().wan_rmsnorm(rows, D, xp, xc, ldx, rp, rc, ldr, gp, eps, hp, ldh, yp, code, ldy, sp,
+    check(load().wan_rmsnorm(_RMSNORM_ARGS.pack(xp, rp, gp, hp, yp, sp, ldx, ldr, ldh, ldy, rows, D, xc, rc, code, eps),
                              _raw_stream(stream, dev)))
     return out, row_scale, (x if residual is None else h_out)
 
@@ -500,7 +515,7 @@ def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_sc
     dev = a.get_device()
     if dev < 0:
         raise ValueError("a is not on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return linear(a, w, bias, activation, residual, a_scale, w_scale, out, out_dtype, stream)
     code = codes.get(a.dtype)
@@ -522,7 +537,7 @@ def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_sc
     ap, lda = _matrix(a, "a", ash, M, dev)
     wp, ldw = _matrix(w, "w", wsh, N, dev)
     op, ldo = _matrix(out, "out", shape, M, dev)
-    per_row, asp, wsp = 0, None, None
+    per_row, asp, wsp = 0, 0, 0
     if code == WAN_FP8:
         if a_scale is None or w_scale is None:
             raise ValueError("e4m3 operands need a_scale and w_scale")
@@ -531,13 +546,13 @@ def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_sc
         wsp = _vector(w_scale, "w_scale", N if per_row else 1, torch.float32, dev)
     elif a_scale is not None or w_scale is not None:
         raise ValueError("bf16 operands have no scales")
-    bp = None if bias is None else _vector(bias, "bias", N, torch.bfloat16, dev)
-    rc, rp, ldr = WAN_F32, None, 0
+    bp = 0 if bias is None else _vector(bias, "bias", N, torch.bfloat16, dev)
+    rc, rp, ldr = WAN_F32, 0, 0
     if residual is not None:
         rc = dtype_code(residual)
         rp, ldr = _matrix(residual, "residual", shape, M, dev)
-    check(load().wan_linear(M, N, K, code, ap, lda, asp, wp, ldw, wsp, per_row, bp, ACTIVATIONS[activation], rp, rc, ldr,
-                            op, dtype_code(out), ldo, _raw_stream(stream, dev)))
+    check(load().wan_linear(_LINEAR_ARGS.pack(ap, wp, asp, wsp, bp, rp, op, lda, ldw, ldr, ldo, M, N, K, code, per_row,
+                                              ACTIVATIONS[activation], rc, dtype_code(out)), _raw_stream(stream, dev)))
     return out
 
 
