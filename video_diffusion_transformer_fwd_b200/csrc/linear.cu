@@ -16,6 +16,13 @@
 // mbarrier; the ring's memory, free once the cluster's products are done), where
 // the same thread adds them in rank order: no workspace, no atomics, and a
 // result that does not depend on timing.
+//
+// A call is launched so that it may start while the kernel before it on the
+// stream still runs, and lets a call after it start early in turn: launch,
+// barrier set-up and TMEM allocation then overlap the last CTAs of the kernel
+// before (one after another 1 x 5120 x 5120 takes 13.2 us, 16.4 without). Every
+// thread passes early_wait() before its first access to global memory, which
+// holds until the kernels before are done and their writes visible.
 #include "common.cuh"
 #include "linear.cuh"
 #include "sm100.cuh"
@@ -37,6 +44,9 @@ constexpr int THREADS = 192;                 // producer, MMA, 4 epilogue warps 
 constexpr int GROUP = 4;                     // tokens that travel and are finished together
 constexpr int GROUP_BYTES = WROWS * GROUP * 4;
 constexpr int SMEM_MAX = 225 * 1024;
+
+__device__ __forceinline__ void early_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void early_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 struct SplitParams {
   int M, N, num_k, split;
@@ -129,7 +139,7 @@ __device__ __forceinline__ void accumulators(uint32_t tmem, int col, int naccs, 
 }
 
 template <bool F8>
-__global__ void __launch_bounds__(THREADS, 3)
+__global__ void __launch_bounds__(THREADS)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                     const SplitParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -148,7 +158,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
   const int groups = (rows + GROUP - 1) / GROUP;
   const int mine = groups > rank ? (groups - rank - 1) / split + 1 : 0;   // groups rank, rank + split, ...
 
-  auto load = [&](int i, int stage) {
+  auto load = [&](int i, int stage) {          // one step of K into a stage
     const uint32_t fb = smem_u32(&full[stage]), dst = smem_u32(smem + stage * stage_bytes);
     mbar_arrive_expect_tx(fb, stage_bytes);
     const int kx = (kb0 + i) * (F8 ? 128 : 64);
@@ -165,6 +175,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     mbar_init(smem_u32(&arrived), 1);
     abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmA);
+    early_wait();
     for (int i = 0; i < ahead; ++i) load(i, i);
     // the other CTAs' sums of this CTA's groups
     mbar_arrive_expect_tx(smem_u32(&arrived), (split - 1) * mine * GROUP_BYTES);
@@ -173,11 +186,13 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     tmem_alloc(smem_u32(&tmem_slot), p.tmem_cols);
     tmem_relinquish();
   }
+  early_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // The cluster's first barrier says that the CTAs' barriers and receive areas
-  // can be written: at once, or when the ring is free.
+  early_next();               // not before the TMEM is there: the next kernel's CTAs may take what is left
+  // Before sums travel, a barrier of the cluster says that every CTA's barriers
+  // and receive area can be written: at once, or when the ring is free.
   const bool early = p.recv != 0;
   if (split > 1 && early) cluster_arrive();
   const uint32_t tmem = tmem_slot;
@@ -220,8 +235,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         const uint32_t d = tmem + acc * p.mt;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {       // 32 bytes of K each: + 2 in 16-byte units
-          if (F8) mma_ss_f8(d, aw + 2 * kk, bt + 2 * kk, p.idesc, (in_chunk | kk) != 0);
-          else mma_ss(d, aw + 2 * kk, bt + 2 * kk, p.idesc, (in_chunk | kk) != 0);
+          const uint32_t add = (in_chunk | kk) != 0;
+          if (F8) mma_ss_f8(d, aw + 2 * kk, bt + 2 * kk, p.idesc, add);
+          else mma_ss(d, aw + 2 * kk, bt + 2 * kk, p.idesc, add);
         }
         tc_commit(smem_u32(&empty[stage]));
         if (++stage == p.stages) { stage = 0; phase ^= 1; }
@@ -306,72 +322,87 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
 }
 
 // ---------------------------------------------------------------- plan
+// How a call is cut up: tokens per tile, K split.
+struct Cut {
+  int mt, split;
+};
 struct Plan {
-  int mt, split, stages, smem, chunk, tmem_cols, recv;
+  Cut c;
+  int stages, smem, chunk, tmem_cols, recv;
 };
 
-int round_up(int v, int m) { return (v + m - 1) / m * m; }
-int recv_bytes(int mt, int split) { return split > 1 ? (mt / GROUP + split - 1) / split * split * GROUP_BYTES : 0; }
 constexpr int SM_SMEM = 228 * 1024, CTA_EXTRA = 1024 + 256;     // of an SM; what a CTA takes besides its ring
 constexpr int SMS = 148;
 
+int round_up(int v, int m) { return (v + m - 1) / m * m; }
+int stage_of(const Cut &c) { return W_BYTES + c.mt * ROW_BYTES; }
+int recv_bytes(const Cut &c) { return c.split > 1 ? (c.mt / GROUP + c.split - 1) / c.split * c.split * GROUP_BYTES : 0; }
+long long ctas_of(const LinArgs &g, const Cut &c) {
+  return (long long)((g.N + WROWS - 1) / WROWS) * c.split * ((g.M + c.mt - 1) / c.mt);
+}
 // CTAs of the grid that share an SM. Clusters do not fill a GPC's SMs to the
 // last one: 1 x 5120 x 5120 in 40 clusters of 7 took 20 us with room for two
 // CTAs per SM (280 of 296), 14 us in clusters of 6 or 8.
-long long ctas_per_sm(long long ctas, int split) {
-  const int sms = split > 1 ? SMS * 7 / 8 : SMS;
-  return (ctas + sms - 1) / sms;
+long long ctas_per_sm(const LinArgs &g, const Cut &c) {
+  const int sms = c.split > 1 ? SMS * 7 / 8 : SMS;
+  return (ctas_of(g, c) + sms - 1) / sms;
 }
-
-long long ctas_of(const LinArgs &g, int mt, int split) {
-  return (long long)((g.N + WROWS - 1) / WROWS) * split * ((g.M + mt - 1) / mt);
+// Accumulators of a CTA. bf16 products are accumulated by the tensor core with
+// a rounding toward zero that grows with the number of steps (relative 1.1e-9
+// K, measured against 64 bits): harmless under a bf16 output, but a float32
+// output gets a new accumulator every 64 steps (4096 of K), added in float32.
+int accumulators_of(const LinArgs &g, int num_k, const Cut &c) {
+  const int nkb = (num_k + c.split - 1) / c.split;
+  return !g.fp8 && g.out_f32 ? std::max(1, std::min((nkb + 63) / 64, 512 / c.mt)) : 1;
+}
+// TMEM columns. CTAs of a cluster wait for one another, so none may wait for
+// TMEM that a CTA of another cluster holds on the same SM. So a CTA takes 128
+// columns, in one size for no gaps between them, and at least a quarter of the
+// SM's shared memory with them, or more columns, and then so much shared memory
+// that no other one fits beside it.
+constexpr int TMEM_SHARE = 128;
+constexpr int SMEM_SHARE = SM_SMEM / 4 - CTA_EXTRA, SMEM_ALONE = SM_SMEM - SM_SMEM / 4;
+int columns_of(const LinArgs &g, int num_k, const Cut &c) {
+  int cols = TMEM_SHARE;
+  while (cols < accumulators_of(g, num_k, c) * c.mt) cols *= 2;
+  return cols;
 }
 // CTAs that an SM holds at once: all of its own while each keeps three stages
-int resident(const LinArgs &g, int mt, int split) {
-  const int fit = SM_SMEM / (3 * (W_BYTES + mt * ROW_BYTES) + 1024 + CTA_EXTRA);
-  return (int)std::min<long long>(std::min(fit, 3), ctas_per_sm(ctas_of(g, mt, split), split));
+int resident(const LinArgs &g, int num_k, const Cut &c) {
+  if (columns_of(g, num_k, c) > TMEM_SHARE) return 1;
+  const int fit = SM_SMEM / (3 * stage_of(c) + 1024 + CTA_EXTRA);
+  return (int)std::min<long long>(std::min(fit, 3), ctas_per_sm(g, c));
 }
 
-Plan make_plan(const LinArgs &g, int num_k, int mt, int split) {
-  const int nkb = (num_k + split - 1) / split;
-  // bf16 products are accumulated by the tensor core with a rounding toward
-  // zero that grows with the number of steps (relative 1.1e-9 K, measured
-  // against 64 bits): harmless under a bf16 output, but a float32 output gets
-  // a new accumulator every 64 steps (4096 of K), added in float32
-  int nacc = !g.fp8 && g.out_f32 ? (nkb + 63) / 64 : 1;
-  nacc = std::min(nacc, 256 / mt);
-  int cols = 32;
-  while (cols < nacc * mt) cols *= 2;
-  const int stage = W_BYTES + mt * ROW_BYTES;
+Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
+  const int nkb = (num_k + c.split - 1) / c.split;
+  const int nacc = accumulators_of(g, num_k, c), cols = columns_of(g, num_k, c);
+  const int stage = stage_of(c);
   // few tokens: a receive area of its own (at most 18 KB) saves a barrier after
   // the products (14.6 -> 13.4 us at 1 x 5120 x 5120); more would cost stages
-  const int own = split > 1 && mt <= 32 ? recv_bytes(mt, split) : 0;
-  const int per_sm = resident(g, mt, split);
-  int stages = (std::min(SM_SMEM / per_sm - CTA_EXTRA, SMEM_MAX) - 1024 - own) / stage;
+  const int own = c.split > 1 && c.mt <= 32 ? recv_bytes(c) : 0;
+  int stages = (std::min(SM_SMEM / resident(g, num_k, c) - CTA_EXTRA, SMEM_MAX) - 1024 - own) / stage;
   stages = std::max(2, std::min(std::min(stages, nkb), MAX_STAGES));
-  int smem = (own ? stages * stage + own : std::max(stages * stage, recv_bytes(mt, split))) + 1024;
-  // CTAs of a cluster wait for one another, so none may wait for TMEM that
-  // another cluster holds: a CTA takes at least the share of the SM's shared
-  // memory that it takes of TMEM (456 bytes a column), and what fits, fits
-  smem = std::max(smem, cols * (SM_SMEM / 512) - CTA_EXTRA);
-  return Plan{mt, split, stages, smem, (nkb + nacc - 1) / nacc, cols, own ? stages * stage : 0};
+  int smem = (own ? stages * stage + own : std::max(stages * stage, recv_bytes(c))) + 1024;
+  smem = std::max(smem, cols > TMEM_SHARE ? SMEM_ALONE : SMEM_SHARE);
+  return Plan{c, stages, smem, (nkb + nacc - 1) / nacc, cols, own ? stages * stage : 0};
 }
 
-// Time of a plan in SM cycles, to compare plans and kernels by: a start and an
+// Time of a cut in SM cycles, to compare cuts and kernels by: a start and an
 // end, what an SM takes in for its CTAs, and a new start for every further wave.
 // Measured: an SM takes in 28 bytes a cycle from HBM (22 with one CTA) and 55
 // from L2 (an operand comes from HBM for the first tile that reads it), and the
 // card 3400 from HBM.
-double split_cost(const LinArgs &g, int num_k, int mt, int split) {
-  const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + mt - 1) / mt;
-  const double per_sm = (double)ctas_per_sm(ctas_of(g, mt, split), split);
-  const int nkb = (num_k + split - 1) / split;
+double split_cost(const LinArgs &g, int num_k, const Cut &c) {
+  const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + c.mt - 1) / c.mt;
+  const double per_sm = (double)ctas_per_sm(g, c);
+  const int nkb = (num_k + c.split - 1) / c.split;
   const double hbm = per_sm > 1.0 ? 28.0 : 22.0;
   auto ingest = [&](double bytes, double readers) { return bytes * (1.0 / hbm / readers + (1.0 - 1.0 / readers) / 55.0); };
-  const double step = ingest(W_BYTES, ntm) + ingest((double)std::min(mt, g.M) * ROW_BYTES, ntn);
+  const double step = ingest(W_BYTES, ntm) + ingest((double)std::min(c.mt, g.M) * ROW_BYTES, ntn);
   const double dram = ((double)g.M + g.N) * g.K * (g.fp8 ? 1 : 2) / 3400.0;
-  return 9500.0 + 10.0 * mt * per_sm + (split > 1 ? 100.0 * split : 0.0) +
-         4000.0 * (ceil(per_sm / resident(g, mt, split)) - 1.0) + std::max(per_sm * nkb * step, dram);
+  return 9500.0 + 10.0 * c.mt * per_sm + (c.split > 1 ? 100.0 * c.split : 0.0) +
+         4000.0 * (ceil(per_sm / resident(g, num_k, c)) - 1.0) + std::max(per_sm * nkb * step, dram);
 }
 // The same of the pair kernel: 256 x 256 tiles in rounds of 74 pairs, 600
 // cycles a step of K or the tile's epilogue (9000 cycles; 20000 where the rows
@@ -386,22 +417,23 @@ double pair_cost(const LinArgs &g, int num_k) {
 // False: the pair kernel.
 bool plan_of(const LinArgs &g, Plan &plan) {
   const int num_k = (g.K + (g.fp8 ? 128 : 64) - 1) / (g.fp8 ? 128 : 64);
-  int best_mt = 0, best_split = 0;
+  Cut cut = {};
   double best = 0.0;
   for (int want = 16; want <= 128; want += 16) {
     if (want > 16 && want - 16 >= g.M) break;
     const int tiles = (g.M + want - 1) / want, mt = round_up((g.M + tiles - 1) / tiles, 16);
     for (int split = 1; split <= std::min(8, num_k); ++split) {
-      const double c = split_cost(g, num_k, mt, split);
-      if (!best_mt || c < best) { best = c; best_mt = mt; best_split = split; }
+      const Cut c = {mt, split};
+      const double cost = split_cost(g, num_k, c);
+      if (!cut.mt || cost < best) { best = cost; cut = c; }
     }
   }
   // the pair kernel keeps one accumulator per tile: not for float32 outputs of
   // bf16 sums longer than 4096 (make_plan)
   const bool chained = !g.fp8 && g.out_f32 && g.K > 4096;
-  const bool fits = (g.M + best_mt - 1) / best_mt <= 65535;
+  const bool fits = (g.M + cut.mt - 1) / cut.mt <= 65535;
   if (!chained && (!fits || pair_cost(g, num_k) < best)) return false;
-  plan = make_plan(g, num_k, best_mt, best_split);
+  plan = make_plan(g, num_k, cut);
   return true;
 }
 
@@ -421,29 +453,37 @@ int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
   int rc;
   if (F8) {
     if ((rc = encode_tmap_2d_u8(&tw, g.w, g.K, g.N, (uint64_t)g.ldw, 128, WROWS))) return rc;
-    if ((rc = encode_tmap_2d_u8(&ta, g.a, g.K, g.M, (uint64_t)g.lda, 128, pl.mt))) return rc;
+    if ((rc = encode_tmap_2d_u8(&ta, g.a, g.K, g.M, (uint64_t)g.lda, 128, pl.c.mt))) return rc;
   } else {
     if ((rc = encode_tmap_2d_bf16(&tw, g.w, g.K, g.N, (uint64_t)g.ldw * 2, 64, WROWS))) return rc;
-    if ((rc = encode_tmap_2d_bf16(&ta, g.a, g.K, g.M, (uint64_t)g.lda * 2, 64, pl.mt))) return rc;
+    if ((rc = encode_tmap_2d_bf16(&ta, g.a, g.K, g.M, (uint64_t)g.lda * 2, 64, pl.c.mt))) return rc;
   }
   SplitParams p = {};
-  p.M = g.M; p.N = g.N; p.num_k = (g.K + (F8 ? 128 : 64) - 1) / (F8 ? 128 : 64); p.split = pl.split;
-  p.mt = pl.mt; p.stages = pl.stages; p.chunk = pl.chunk; p.recv = pl.recv; p.tmem_cols = pl.tmem_cols;
-  p.idesc = F8 ? idesc_e4m3(WROWS, pl.mt) : idesc_bf16(WROWS, pl.mt, 0);
+  p.M = g.M; p.N = g.N; p.num_k = (g.K + (F8 ? 128 : 64) - 1) / (F8 ? 128 : 64); p.split = pl.c.split;
+  p.mt = pl.c.mt; p.stages = pl.stages; p.chunk = pl.chunk; p.recv = pl.recv; p.tmem_cols = pl.tmem_cols;
+  p.idesc = F8 ? idesc_e4m3(WROWS, pl.c.mt) : idesc_bf16(WROWS, pl.c.mt, 0);
   p.e = lin_epilogue(g);
   p.watchdog = watchdog_ptr();
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = pl.split; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)((g.N + WROWS - 1) / WROWS * pl.split), (unsigned)((g.M + pl.mt - 1) / pl.mt), 1);
+  attr[0].val.clusterDim.x = pl.c.split; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  const int tiles = (g.M + pl.c.mt - 1) / pl.c.mt;
+  cfg.gridDim = dim3((unsigned)(ctas_of(g, pl.c) / tiles), (unsigned)tiles, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   WAN_TRY_CUDA(cudaLaunchKernelEx(&cfg, linear_split_kernel<F8>, tw, ta, p), "linear launch");
   return WAN_OK;
+}
+
+int launch_plan(const LinArgs &g, const Plan &pl, cudaStream_t s) {
+  if ((g.M + pl.c.mt - 1) / pl.c.mt > 65535) return set_error(WAN_EINVAL, "linear: M=%d too large", g.M);
+  return g.fp8 ? launch<true>(g, pl, s) : launch<false>(g, pl, s);
 }
 }  // namespace
 
@@ -463,9 +503,7 @@ int launch_linear(const LinArgs &g, cudaStream_t s) {
     k = Known{g.M, g.N, g.K, kind, false, Plan{}};
     k.split = plan_of(g, k.plan);
   }
-  if (!k.split) return gemm_tc_linear(g, s);
-  if ((g.M + k.plan.mt - 1) / k.plan.mt > 65535) return set_error(WAN_EINVAL, "linear: M=%d too large", g.M);
-  return g.fp8 ? launch<true>(g, k.plan, s) : launch<false>(g, k.plan, s);
+  return k.split ? launch_plan(g, k.plan, s) : gemm_tc_linear(g, s);
 }
 
 }  // namespace wan

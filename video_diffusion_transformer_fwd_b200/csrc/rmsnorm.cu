@@ -377,11 +377,8 @@ template <typename XT, typename RT, bool RES, typename YT, int NV, int TPR>
 int rms_launch(const RmsArgs &a, RowLayout lay, int threads, cudaStream_t s) {
   const int per = TPR ? threads / TPR : 1;
   const long long grid = ((long long)a.rows + per - 1) / per;
-  if (lay == ROWS_ALIGNED) {
-    rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, false><<<(unsigned)grid, threads, 0, s>>>(a);
-  } else {
-    rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, true><<<(unsigned)grid, threads, 0, s>>>(a);
-  }
+  if (lay == ROWS_ALIGNED) rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, false><<<(unsigned)grid, threads, 0, s>>>(a);
+  else rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, true><<<(unsigned)grid, threads, 0, s>>>(a);
   WAN_CHECK_LAUNCH("rmsnorm");
   return WAN_OK;
 }
