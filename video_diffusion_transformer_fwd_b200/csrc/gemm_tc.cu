@@ -59,11 +59,12 @@ constexpr int STG_BYTES = 32 * 32 * 4;  // one warp's 32 x 32 fp32 staging tile 
 constexpr bool USE_WIDE = true;          // 256 x 512 tiles wherever the shape allows
 
 // Tile geometry of the two variants. LIN (wan_linear): the narrow tile with
-// twice the epilogue warps, each on 128 columns with two staging tiles.
+// twice the epilogue warps, each with two staging tiles; its width (a multiple
+// of 32 up to BN) and with it the stages are the launch's.
 template <bool WIDE, bool LIN = false>
 struct Geo {
   static constexpr int BN = WIDE ? 512 : 256;              // output columns per pair tile
-  static constexpr int STAGES = WIDE ? 4 : LIN ? 5 : 6;
+  static constexpr int STAGES = WIDE ? 4 : LIN ? 8 : 6;    // LIN: at most
   static constexpr int B_BYTES = (BN / 2) * BK * 2;        // this CTA's half of B
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int EPI_WARPS = (WIDE ? 8 : 4) * (LIN ? 2 : 1);
@@ -71,7 +72,7 @@ struct Geo {
   static constexpr int NACC = WIDE ? 1 : 2;                // TMEM accumulators (BN columns each)
   static constexpr int NSTG = WIDE ? 1 : 2;                // residual staging tiles per epilogue warp
   static constexpr int EPI_SMEM = EPI_WARPS * NSTG * STG_BYTES;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_SMEM + 256;
+  static constexpr int SMEM_BYTES = LIN ? 232448 : 1024 + STAGES * STAGE_BYTES + EPI_SMEM + 256;
   static_assert(!(WIDE && LIN), "wan_linear runs the narrow tile");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(8 * (2 * STAGES + 4) + 16 + 8 * EPI_WARPS <= 256, "barriers");
@@ -93,7 +94,13 @@ struct TcParams {
   int *watchdog;
   const void *ss_hi; int *dbg;            // debug bounds checks: end of ss
   LinEpilogue lin;                        // EPI_LINEAR
+  int bn, stages; uint32_t idesc;         // EPI_LINEAR: columns of a pair tile
 };
+// stages of wan_linear's ring for tiles of bn columns
+constexpr int lin_stages(int bn) {
+  const int n = (Geo<false, true>::SMEM_BYTES - 1024 - 256 - Geo<false, true>::EPI_SMEM) / (A_BYTES + bn / 2 * 128);
+  return n < Geo<false, true>::STAGES ? n : Geo<false, true>::STAGES;
+}
 
 __device__ __forceinline__ void tile_coords(int t, const TcParams &p, int &mb, int &nb) {
   const int group = GROUP_M * p.num_n;
@@ -119,14 +126,14 @@ __device__ __forceinline__ float bf16_bits_to_float(uint32_t lo16) {
   return __uint_as_float(lo16 << 16);
 }
 
-// wan_linear's epilogue: warp `ew` of 8 takes 128 columns of 32 rows of every
-// tile of its pair, 32 columns at a time, one thread per row: scales, bias,
-// activation, residual, output. Residual and output pass through two 4 KB
-// shared-memory tiles of the warp (128-byte rows of 32 float32 or 64 bf16,
-// 16-byte group g of row r at g ^ (r & 7)) and the TMA unit, which keeps the
-// warp's own loads and stores to shared memory: a version that stored rows of
-// 32 bytes from registers held the 7800 x 8960 x 1536 product at 182 us, its
-// products alone take 141 us. The residual of a chunk is asked for when the
+// wan_linear's epilogue: 8 warps, two for each 32 rows of a tile, take its
+// chunks of 32 columns in turn, one thread per row: scales, bias, activation,
+// residual, output. Residual and output pass through two 4 KB shared-memory
+// tiles of the warp (float32: 128-byte rows, 16-byte group g of row r at
+// g ^ (r & 7); bf16: 64-byte rows, at g ^ (r / 2 & 3)) and the TMA unit, which
+// keeps the warp's own loads and stores to shared memory: a version that stored
+// rows of 32 bytes from registers held the 7800 x 8960 x 1536 product at 182 us,
+// its products alone take 141 us. The residual of a chunk is asked for when the
 // chunk before it has been added, the first one of a tile during the last of
 // the tile before. Outputs (or residuals) whose rows do not start on 16-byte
 // boundaries are turned around in shared memory instead and stored a column
@@ -140,44 +147,43 @@ struct LinearEpilogue {
   uint8_t *tiles;               // this warp's two staging tiles
   uint32_t rbar;                // counts the bytes of a residual tile
   volatile int *abort_flag;
-  int hcol, q, lane, rank, pair, npairs;
+  int half, q, lane, rank, pair, npairs;      // half: takes chunks half, half + 2, ...
   bool tma_res;
-  // the residual tile asked for last: pair tile rt, unit ru (units of 128 bytes a row)
-  int rt, ru, asked = 0, taken = 0;
+  // the residual chunk asked for last: pair tile rt, chunk rc
+  int rt, rc, asked = 0, taken = 0;
 
-  __device__ __forceinline__ int res_cols() const { return e.res_f32 ? 32 : 64; }
   __device__ __forceinline__ void corner(int t, int &m0, int &n0) const {
     int mb, nb;
     tile_coords(t, p, mb, nb);
     m0 = mb * 2 * BM + rank * BM + q * 32;
-    n0 = nb * G::BN + hcol;
+    n0 = nb * p.bn;
   }
-  // ask for the residual unit after (rt, ru); units outside the matrix are passed over
+  // ask for the residual chunk after (rt, rc); chunks outside the matrix are passed over
   __device__ __forceinline__ void ask_next() {
     int m0, n0;
-    for (++ru; rt < p.num_tiles; rt += npairs, ru = 0) {
+    for (rc += 2; rt < p.num_tiles; rt += npairs, rc = half) {
       corner(rt, m0, n0);
-      if (m0 < p.M && n0 + ru * res_cols() < p.N && ru * res_cols() < 128) break;
+      if (m0 < p.M && 32 * rc < p.bn && n0 + 32 * rc < p.N) break;
     }
     if (rt >= p.num_tiles) return;
     if (lane == 0) {
-      mbar_arrive_expect_tx(rbar, STG_BYTES);
-      tma_load_2d(smem_u32(tiles), tmR, n0 + ru * res_cols(), m0, rbar);
+      mbar_arrive_expect_tx(rbar, e.res_f32 ? STG_BYTES : STG_BYTES / 2);
+      tma_load_2d(smem_u32(tiles), tmR, n0 + 32 * rc, m0, rbar);
     }
     ++asked;
   }
-  __device__ __forceinline__ uint8_t *slot(uint8_t *tile, int row, int g) const {
+  __device__ __forceinline__ uint8_t *slot(uint8_t *tile, int row, int g) const {       // of a float32 tile
     return tile + row * 128 + ((g ^ (row & 7)) << 4);
   }
+  __device__ __forceinline__ uint8_t *slot16(uint8_t *tile, int row, int g) const {     // of a bf16 tile
+    return tile + row * 64 + ((g ^ ((row >> 1) & 3)) << 4);
+  }
 
-  // v += the residual of chunk c
-  __device__ __forceinline__ bool add_residual(float (&v)[32], int c, bool last) {
-    const bool fresh = e.res_f32 || !(c & 1);
-    if (fresh) {
-      const bool ok = mbar_wait(rbar, taken & 1, abort_flag, p.watchdog, 0x123);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      ++taken;
-    }
+  // v += the residual of the chunk
+  __device__ __forceinline__ bool add_residual(float (&v)[32]) {
+    const bool ok = mbar_wait(rbar, taken & 1, abort_flag, p.watchdog, 0x123);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    ++taken;
     if (e.res_f32) {
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
@@ -187,7 +193,7 @@ struct LinearEpilogue {
     } else {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(slot(tiles, lane, 4 * (c & 1) + g));
+        const uint4 x = *reinterpret_cast<const uint4 *>(slot16(tiles, lane, g));
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -197,7 +203,7 @@ struct LinearEpilogue {
       }
     }
     __syncwarp();                                // the tile has been read
-    if (e.res_f32 || (c & 1) || last) ask_next();
+    ask_next();
     return true;
   }
 
@@ -226,7 +232,7 @@ struct LinearEpilogue {
     const bool tma_out = e.vec_out;
     tma_res = e.res && e.vec_res;
     int stores = 0;
-    rt = pair; ru = -1;
+    rt = pair; rc = half - 2;
     if (tma_res) ask_next();
     int i = 0;
     for (int t = pair; t < p.num_tiles; t += npairs, ++i) {
@@ -235,8 +241,8 @@ struct LinearEpilogue {
       corner(t, m0, n0);
       const int m = m0 + lane;
       // Per-column operands, read while the tile's products run: lane l holds
-      // columns 8 (l % 16) .. + 7 of the warp's 128, taken by shuffles.
-      const int c0 = n0 + 8 * (lane & 15);
+      // columns 8 l .. 8 l + 7 of the tile, taken by shuffles.
+      const int c0 = n0 + 8 * lane;
       uint4 bias8 = make_uint4(0u, 0u, 0u, 0u);
       float4 s_lo = make_float4(1.f, 1.f, 1.f, 1.f), s_hi = s_lo;
       const bool rows = F8 && e.w_scale_rows;
@@ -263,19 +269,19 @@ struct LinearEpilogue {
       const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i >> 1) & 1, abort_flag, p.watchdog, 0x122);
       if (!__all_sync(0xffffffffu, ready)) break;
       tc_fence_after();
+      const int chunks = p.bn / 32;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = half; c < chunks; c += 2) {
         uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + buf * G::BN + hcol + c * 32, r);
+        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + buf * G::BN + c * 32, r);
         tmem_ld_wait();
-        if (c == 3) {
+        if (c + 2 >= chunks) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(buf ? free1 : free0);
         }
         const int n = n0 + c * 32;
         if (m0 >= p.M || n >= p.N) continue;     // warp-uniform
-        const bool last = c == 3 || n + 32 >= p.N;
         float v[32];
 #pragma unroll
         for (int j4 = 0; j4 < 4; ++j4) {         // columns 8 j4 .. of the chunk: lane 4 c + j4
@@ -299,16 +305,14 @@ struct LinearEpilogue {
           }
         }
         lin_act_row(v, e.act);
-        if (tma_res && !add_residual(v, c, last)) return;
+        if (tma_res && !add_residual(v)) return;
         if (!tma_out || (e.res && !tma_res)) { store_by_columns(v, m0, n); continue; }
         // with a residual the second tile alone holds the output, else both in turn
         uint8_t *tile = tiles + (e.res || (stores & 1) ? STG_BYTES : 0);
-        if (e.out_f32 || !(c & 1)) {
-          if (lane == 0) {                       // this tile's previous store has read it
-            if (e.res) bulk_wait_group_read<0>(); else bulk_wait_group_read<1>();
-          }
-          __syncwarp();
+        if (lane == 0) {                         // this tile's previous store has read it
+          if (e.res) bulk_wait_group_read<0>(); else bulk_wait_group_read<1>();
         }
+        __syncwarp();
         if (e.out_f32) {
 #pragma unroll
           for (int g = 0; g < 8; ++g)
@@ -320,18 +324,16 @@ struct LinearEpilogue {
                                          __floats2bfloat162_rn(v[8 * g + 2], v[8 * g + 3]),
                                          __floats2bfloat162_rn(v[8 * g + 4], v[8 * g + 5]),
                                          __floats2bfloat162_rn(v[8 * g + 6], v[8 * g + 7])};
-            *reinterpret_cast<uint4 *>(slot(tile, lane, 4 * (c & 1) + g)) = *reinterpret_cast<const uint4 *>(h);
+            *reinterpret_cast<uint4 *>(slot16(tile, lane, g)) = *reinterpret_cast<const uint4 *>(h);
           }
         }
-        if (e.out_f32 || (c & 1) || last) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(tmX, smem_u32(tile), e.out_f32 ? n : n0 + (c & ~1) * 32, m0);
-            bulk_commit_group();
-          }
-          ++stores;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(tmX, smem_u32(tile), n, m0);
+          bulk_commit_group();
         }
+        ++stores;
       }
     }
   }
@@ -348,7 +350,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmB2,
                const __grid_constant__ CUtensorMap tmX, const TcParams p) {
   using G = Geo<WIDE, EPI == EPI_LINEAR>;
-  constexpr int BN = G::BN, STAGES = G::STAGES, B_BYTES = G::B_BYTES, STAGE_BYTES = G::STAGE_BYTES;
+  constexpr bool LIN = EPI == EPI_LINEAR;
+  const int BN = LIN ? p.bn : G::BN, STAGES = LIN ? p.stages : G::STAGES;
+  const int B_BYTES = LIN ? p.bn / 2 * 128 : G::B_BYTES, STAGE_BYTES = A_BYTES + B_BYTES;
   constexpr int NACC = G::NACC, NSTG = G::NSTG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -409,23 +413,21 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int fills[STAGES];
-#pragma unroll
-      for (int st = 0; st < STAGES; ++st) fills[st] = 0;
-      bool ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
-        int mb, nb;
-        tile_coords(t, p, mb, nb);
-        const int n0 = nb * BN;
-        const int seg = n0 / p.segN;
-        const CUtensorMap *bm = seg == 0 ? &tmB0 : (seg == 1 ? &tmB1 : &tmB2);
-        const int a_row = mb * 2 * BM + (int)rank * BM;
-        const int b_row = n0 - seg * p.segN + (int)rank * 128;   // this CTA's 128 rows of each N = 256 half
-        for (int kb = 0; kb < p.num_k; ++kb) {
-          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101)) { ok = false; break; }
+    int stage = 0;
+    uint32_t phase = 0;
+    long long loads = 0;
+    bool ok = true;
+    for (int t = pair; t < p.num_tiles && ok; t += npairs) {
+      int mb, nb;
+      tile_coords(t, p, mb, nb);
+      const int n0 = nb * BN;
+      const int seg = n0 / p.segN;
+      const CUtensorMap *bm = seg == 0 ? &tmB0 : (seg == 1 ? &tmB1 : &tmB2);
+      const int a_row = mb * 2 * BM + (int)rank * BM;
+      const int b_row = n0 - seg * p.segN + (int)rank * (LIN ? BN / 2 : 128);   // this CTA's rows of each N = 256 half (of bn)
+      for (int kb = 0; kb < p.num_k; ++kb) {
+        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101)) { ok = false; break; }
+        if (elect_one()) {
           const uint32_t fb_local = smem_u32(&full[stage]);
           if (leader) mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
           const uint32_t fb = mapa_shared(fb_local, 0);
@@ -434,22 +436,25 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           tma_load_2d_pair(smem_u32(sB + stage * B_BYTES), bm, kx, b_row, fb);
           if (WIDE)      // the second N = 256 half of the tile: B rows 256 further
             tma_load_2d_pair(smem_u32(sB + stage * B_BYTES + B_BYTES / 2), bm, kx, b_row + 256, fb);
-          ++fills[stage];
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
-      }
-      // drain (leader): every issued copy of the pair has landed before exit.
-      // The peer's copies complete on the leader's barrier, so the leader's
-      // drain also covers them; the final cluster barrier orders the rest.
-      if (leader) {
-        int never = 0;
-        for (int s = 0; s < STAGES; ++s)
-          if (fills[s] > 0) mbar_wait(smem_u32(&full[s]), (fills[s] - 1) & 1, &never, p.watchdog, 0x102);
+        ++loads;
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     }
+    // drain (leader): every issued copy of the pair has landed before exit.
+    // The peer's copies complete on the leader's barrier, so the leader's
+    // drain also covers them; the final cluster barrier orders the rest.
+    if (leader && lane == 0) {
+      int never = 0;
+      for (int s = 0; s < STAGES; ++s) {
+        const long long fills = loads > s ? (loads - 1 - s) / STAGES + 1 : 0;
+        if (fills > 0) mbar_wait(smem_u32(&full[s]), (uint32_t)((fills - 1) & 1), &never, p.watchdog, 0x102);
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader only)
-    if (lane == 0 && leader) {
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0;
       int i = 0;
@@ -459,7 +464,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t acc_phase = (i / NACC) & 1;
         if (!mbar_wait(smem_u32(&tempty[buf]), acc_phase ^ 1, abort_flag, p.watchdog, 0x111)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + buf * BN;
+        const uint32_t d = tmem_base + buf * G::BN;
         for (int kb = 0; kb < p.num_k; ++kb) {
           if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112)) { ok = false; break; }
           tc_fence_after();
@@ -467,35 +472,32 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           const uint64_t b0 = desc_kmajor_sw128(smem_u32(sB + stage * B_BYTES));
           // 4 MMAs of 32 bytes of K per stage (16 bf16 or 32 e4m3 each):
           // the descriptor start address advances 32 bytes (2 in 16-byte units)
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < BN / 256; ++h) {
-            // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
-            const uint64_t bh = b0 + (uint64_t)((h * (B_BYTES / 2)) >> 4);
+            for (int h = 0; h < G::BN / 256; ++h) {
+              // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
+              const uint64_t bh = b0 + (uint64_t)((h * (B_BYTES / 2)) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              if (F8)
-                mma_ss_pair_f8(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, IDESC8, (kb | kk) != 0);
-              else
-                mma_ss_pair(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, IDESC, (kb | kk) != 0);
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                if (F8)
+                  mma_ss_pair_f8(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (kb | kk) != 0);
+                else
+                  mma_ss_pair(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (kb | kk) != 0);
+              }
             }
+            tc_commit_both(smem_u32(&empty[stage]));
           }
-          const uint32_t eb = smem_u32(&empty[stage]);
-          tc_commit_pair(eb);
-          tc_commit_pair(mapa_shared(eb, 1));
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
-        if (ok) {
-          const uint32_t fb = smem_u32(&tfull[buf]);
-          tc_commit_pair(fb);
-          tc_commit_pair(mapa_shared(fb, 1));
-        }
+        if (ok && elect_one()) tc_commit_both(smem_u32(&tfull[buf]));
       }
     }
+    __syncwarp();
   } else if (EPI == EPI_LINEAR) {
     if constexpr (EPI == EPI_LINEAR) {
       const int ew = warp - 2;
       LinearEpilogue<F8> le{p, p.lin, &tmX, &tmB1, sE + ew * NSTG * STG_BYTES, smem_u32(&rbars[ew]), abort_flag,
-                            128 * (ew >> 2), warp & 3, lane, (int)rank, pair, npairs};
+                            ew >> 2, warp & 3, lane, (int)rank, pair, npairs};
       le.run(tmem_base, tfull, tempty);
       le.drain();
     }
@@ -800,32 +802,35 @@ int launch_epi(int epi, const CUtensorMap &ta, const CUtensorMap *tb, const CUte
 }
 }  // namespace
 
-// wan_linear on CTA pairs: the same products with wan_linear's epilogue. K may
-// end inside a step and N inside a tile (the TMA unit fills zeros).
-int gemm_tc_linear(const LinArgs &g, cudaStream_t s) {
+// wan_linear on CTA pairs: the same products with wan_linear's epilogue, in
+// tiles of 256 rows and bn columns. K may end inside a step and N inside a tile
+// (the TMA unit fills zeros).
+int gemm_tc_linear(const LinArgs &g, int bn, cudaStream_t s) {
   CUtensorMap ta, tb[3], tx;
   const int bk = g.fp8 ? BK8 : BK;
   int rc;
   if (g.fp8) {
     if ((rc = encode_tmap_2d_u8(&ta, g.a, g.K, g.M, (uint64_t)g.lda, BK8, BM))) return rc;
-    if ((rc = encode_tmap_2d_u8(&tb[0], g.w, g.K, g.N, (uint64_t)g.ldw, BK8, 128))) return rc;
+    if ((rc = encode_tmap_2d_u8(&tb[0], g.w, g.K, g.N, (uint64_t)g.ldw, BK8, bn / 2))) return rc;
   } else {
     if ((rc = encode_tmap_2d_bf16(&ta, g.a, g.K, g.M, (uint64_t)g.lda * 2, BK, BM))) return rc;
-    if ((rc = encode_tmap_2d_bf16(&tb[0], g.w, g.K, g.N, (uint64_t)g.ldw * 2, BK, 128))) return rc;
+    if ((rc = encode_tmap_2d_bf16(&tb[0], g.w, g.K, g.N, (uint64_t)g.ldw * 2, BK, bn / 2))) return rc;
   }
   TcParams p = {};
   p.lin = lin_epilogue(g);
   tb[1] = tb[2] = tx = tb[0];                     // maps that no copy uses stay valid ones
-  auto rows32 = [&](CUtensorMap *t, const void *base, long long ld, bool f32) {
+  auto chunks = [&](CUtensorMap *t, const void *base, long long ld, bool f32) {      // 32 x 32 boxes
     return f32 ? encode_tmap_2d_f32(t, base, g.N, g.M, (uint64_t)ld * 4, 32, 32)
-               : encode_tmap_2d_bf16(t, base, g.N, g.M, (uint64_t)ld * 2, 64, 32);
+               : encode_tmap_2d_bf16_sw64(t, base, g.N, g.M, (uint64_t)ld * 2, 32, 32);
   };
-  if (p.lin.vec_out && (rc = rows32(&tx, g.out, g.ldo, g.out_f32))) return rc;
-  if (g.res && p.lin.vec_res && (rc = rows32(&tb[1], g.res, g.ldr, g.res_f32))) return rc;
+  if (p.lin.vec_out && (rc = chunks(&tx, g.out, g.ldo, g.out_f32))) return rc;
+  if (g.res && p.lin.vec_res && (rc = chunks(&tb[1], g.res, g.ldr, g.res_f32))) return rc;
   p.M = g.M; p.N = g.N; p.K = g.K;
-  p.segN = (g.N + 255) / 256 * 256;               // one weight segment
+  p.bn = bn; p.stages = lin_stages(bn);
+  p.idesc = g.fp8 ? idesc_e4m3(2 * BM, bn) : idesc_bf16(2 * BM, bn, 0);
   p.num_m = (g.M + 2 * BM - 1) / (2 * BM);
-  p.num_n = (g.N + 255) / 256;
+  p.num_n = (g.N + bn - 1) / bn;
+  p.segN = p.num_n * bn;                          // one weight segment
   if ((long long)p.num_m * p.num_n > 0x3fffffff) return set_error(WAN_EINVAL, "linear: M=%d N=%d too large", g.M, g.N);
   p.num_tiles = p.num_m * p.num_n;
   p.num_k = (g.K + bk - 1) / bk;

@@ -199,15 +199,15 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
+    int stage = ahead == p.stages ? 0 : ahead, issued = ahead;
+    uint32_t phase = 0;
+    for (; issued < nkb; ++issued) {
+      if (!mbar_wait(smem_u32(&empty[stage]), phase, &abort_flag, p.watchdog, 0x201)) break;
+      if (elect_one()) load(issued, stage);
+      if (++stage == p.stages) { stage = 0; phase ^= 1; }
+    }
+    // every copy issued has landed before the CTA ends
     if (lane == 0) {
-      int stage = ahead == p.stages ? 0 : ahead, issued = ahead;
-      uint32_t phase = 0;
-      for (; issued < nkb; ++issued) {
-        if (!mbar_wait(smem_u32(&empty[stage]), phase, &abort_flag, p.watchdog, 0x201)) break;
-        load(issued, stage);
-        if (++stage == p.stages) { stage = 0; phase ^= 1; }
-      }
-      // every copy issued has landed before the CTA ends
       int never = 0;
       for (int s = 0; s < p.stages; ++s) {
         const int fills = issued > s ? (issued - 1 - s) / p.stages + 1 : 0;
@@ -222,29 +222,32 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int i = 0, in_chunk = 0, acc = 0; i < nkb; ++i) {
-        if (!mbar_wait(smem_u32(&full[stage]), phase, &abort_flag, p.watchdog, 0x211)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t base = smem_u32(smem + stage * stage_bytes);
-        const uint64_t aw = desc_kmajor_sw128(base);
-        const uint64_t bt = desc_kmajor_sw128(base + W_BYTES);
-        const uint32_t d = tmem + acc * p.mt;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t ring = smem_u32(smem), f0 = smem_u32(full);
+    bool next = mbar_try_wait(f0, 0);
+    for (int i = 0, in_chunk = 0, acc = 0; i < nkb; ++i) {
+      if (!next && !mbar_wait(f0 + 8 * stage, phase, &abort_flag, p.watchdog, 0x211)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t base = ring + stage * stage_bytes;
+      const uint64_t aw = desc_kmajor_sw128(base);
+      const uint64_t bt = desc_kmajor_sw128(base + W_BYTES);
+      const uint32_t d = tmem + acc * p.mt, eb = smem_u32(empty) + 8 * stage;
+      if (++stage == p.stages) { stage = 0; phase ^= 1; }
+      next = i + 1 < nkb && mbar_try_wait(f0 + 8 * stage, phase);     // asked ahead of the products' issue
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {       // 32 bytes of K each: + 2 in 16-byte units
           const uint32_t add = (in_chunk | kk) != 0;
           if (F8) mma_ss_f8(d, aw + 2 * kk, bt + 2 * kk, p.idesc, add);
           else mma_ss(d, aw + 2 * kk, bt + 2 * kk, p.idesc, add);
         }
-        tc_commit(smem_u32(&empty[stage]));
-        if (++stage == p.stages) { stage = 0; phase ^= 1; }
-        if (++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
+        tc_commit(eb);
       }
-      if (ok) tc_commit(smem_u32(&done));
+      if (++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
     }
+    if (ok && elect_one()) tc_commit(smem_u32(&done));
     __syncwarp();
     if (split > 1) {
       if (!early) cluster_arrive();
@@ -404,24 +407,32 @@ double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   return 9500.0 + 10.0 * c.mt * per_sm + (c.split > 1 ? 100.0 * c.split : 0.0) +
          4000.0 * (ceil(per_sm / resident(g, num_k, c)) - 1.0) + std::max(per_sm * nkb * step, dram);
 }
-// The same of the pair kernel: 256 x 256 tiles in rounds of 74 pairs, 600
-// cycles a step of K or the tile's epilogue (9000 cycles; 20000 where the rows
-// of out or residual are out of the TMA unit's reach), the last one in the open.
-double pair_cost(const LinArgs &g, int num_k) {
-  const double tiles = ceil(g.M / 256.0) * ceil(g.N / 256.0);
+// The same of the pair kernel: tiles of 256 x bn in rounds of 74 pairs. A step
+// of K takes what its operands' way through shared memory takes (written,
+// read, and B read for the other CTA of the pair too, at 128 bytes a cycle: 640
+// cycles at bn = 256, 512 of them the products'), a tile no less than its
+// epilogue (9000 cycles at bn = 256; 20000 where the rows of out or residual
+// are out of the TMA unit's reach); the last one is in the open.
+double pair_cost(const LinArgs &g, int num_k, int bn) {
+  const double tiles = ceil(g.M / 256.0) * ceil(g.N / (double)bn);
   const LinEpilogue e = lin_epilogue(g);
-  const double epi = e.vec_out && e.vec_res ? 9000.0 : 20000.0;
-  return 8000.0 + epi + ceil(tiles / 74.0) * std::max(num_k * 600.0, epi);
+  const double epi = (e.vec_out && e.vec_res ? 9000.0 : 20000.0) * bn / 256.0;
+  return 8000.0 + epi + ceil(tiles / 74.0) * std::max(num_k * (256.0 + 1.5 * bn), epi);
 }
 
-// False: the pair kernel.
-bool plan_of(const LinArgs &g, Plan &plan) {
+// The kernel of a call: pair_bn != 0 for the pair kernel, else the plan.
+struct Choice {
+  int pair_bn;
+  Plan plan;
+};
+Choice choose(const LinArgs &g) {
   const int num_k = (g.K + (g.fp8 ? 128 : 64) - 1) / (g.fp8 ? 128 : 64);
   Cut cut = {};
   double best = 0.0;
   for (int want = 16; want <= 128; want += 16) {
     if (want > 16 && want - 16 >= g.M) break;
     const int tiles = (g.M + want - 1) / want, mt = round_up((g.M + tiles - 1) / tiles, 16);
+    if (tiles > 65535) continue;
     for (int split = 1; split <= std::min(8, num_k); ++split) {
       const Cut c = {mt, split};
       const double cost = split_cost(g, num_k, c);
@@ -429,12 +440,15 @@ bool plan_of(const LinArgs &g, Plan &plan) {
     }
   }
   // the pair kernel keeps one accumulator per tile: not for float32 outputs of
-  // bf16 sums longer than 4096 (make_plan)
-  const bool chained = !g.fp8 && g.out_f32 && g.K > 4096;
-  const bool fits = (g.M + cut.mt - 1) / cut.mt <= 65535;
-  if (!chained && (!fits || pair_cost(g, num_k) < best)) return false;
-  plan = make_plan(g, num_k, cut);
-  return true;
+  // bf16 sums longer than 4096 (accumulators_of)
+  int bn = 0;
+  if (!cut.mt || g.fp8 || !g.out_f32 || g.K <= 4096) {
+    for (int n = 256; n >= 96; n -= 32) {
+      const double cost = pair_cost(g, num_k, n);
+      if ((!cut.mt && !bn) || cost < best) { best = cost; bn = n; }
+    }
+  }
+  return bn ? Choice{bn, Plan{}} : Choice{0, make_plan(g, num_k, cut)};
 }
 
 template <bool F8>
@@ -482,7 +496,6 @@ int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
 }
 
 int launch_plan(const LinArgs &g, const Plan &pl, cudaStream_t s) {
-  if ((g.M + pl.c.mt - 1) / pl.c.mt > 65535) return set_error(WAN_EINVAL, "linear: M=%d too large", g.M);
   return g.fp8 ? launch<true>(g, pl, s) : launch<false>(g, pl, s);
 }
 }  // namespace
@@ -491,8 +504,7 @@ int launch_linear(const LinArgs &g, cudaStream_t s) {
   // the choice costs a few microseconds of the host: the last ones are kept, by sizes and types
   struct Known {
     int M, N, K, kind;
-    bool split;
-    Plan plan;
+    Choice choice;
   };
   thread_local Known known[32] = {};
   const LinEpilogue e = lin_epilogue(g);
@@ -500,10 +512,9 @@ int launch_linear(const LinArgs &g, cudaStream_t s) {
   const unsigned h = ((unsigned)g.M * 2654435761u ^ (unsigned)g.N * 40503u ^ (unsigned)g.K * 65599u ^ (unsigned)kind) >> 3;
   Known &k = known[h % 32];
   if (k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
-    k = Known{g.M, g.N, g.K, kind, false, Plan{}};
-    k.split = plan_of(g, k.plan);
+    k = Known{g.M, g.N, g.K, kind, choose(g)};
   }
-  return k.split ? launch_plan(g, k.plan, s) : gemm_tc_linear(g, s);
+  return k.choice.pair_bn ? gemm_tc_linear(g, k.choice.pair_bn, s) : launch_plan(g, k.choice.plan, s);
 }
 
 }  // namespace wan

@@ -89,6 +89,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   return ok;
 }
 
+// One thread of a converged warp. A loop that issues TMA or tcgen05 work runs in
+// all lanes with only the issue itself under elect_one(): its operands then
+// stay in uniform registers. Inside `if (lane == 0)` each of them is moved
+// there lane by lane (four tcgen05.mma took 224 cycles to issue, 99 this way).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Bring the line holding `p` into L1 (a hint: no register, no wait).
 __device__ __forceinline__ void prefetch_l1(const void *p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
@@ -261,6 +271,11 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar_cluster) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                ::"r"(bar_cluster) : "memory");
 }
+// The same on the mbarrier at this offset in both CTAs of the pair.
+__device__ __forceinline__ void tc_commit_both(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
 // Pair MMA (issued by the leader CTA): D (M=256 split 128/128 across the
 // pair's TMEM) (+)= A (128 rows from each CTA's smem) * B (N split in halves
 // across the two CTAs' smem).
@@ -377,6 +392,9 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // Host side: cuTensorMapEncodeTiled fetched through the runtime (no libcuda link).
 int encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
+// 64-byte rows (box_inner 32): 16-byte group g of row r at g ^ (r / 2 % 4)
+int encode_tmap_2d_bf16_sw64(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
 int encode_tmap_2d_u8(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                       uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
 int encode_tmap_2d_f32(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,

@@ -25,7 +25,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 }
 
 static int encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner,
-                     uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows) {
+                     uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = get_encode();
   if (!enc) return set_error(WAN_ECUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t gdim[2] = {inner, rows};
@@ -33,7 +34,7 @@ static int encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base,
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(map, dt, 2, const_cast<void *>(base), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(WAN_ECUDA, "cuTensorMapEncodeTiled (2d) failed: %d", (int)r);
   return WAN_OK;
 }
@@ -41,6 +42,12 @@ static int encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base,
 int encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows) {
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, rows, row_stride_bytes, box_inner, box_rows);
+}
+
+int encode_tmap_2d_bf16_sw64(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, rows, row_stride_bytes, box_inner, box_rows,
+                   CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int encode_tmap_2d_u8(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
