@@ -137,7 +137,8 @@ def test_workload_sizes(M, N, K, f8):
     assert float((got.float() - ref).norm() / ref.norm()) <= 2.0 ** -8
 
 
-@pytest.mark.parametrize("M,N,K", [(16, 64, 16384), (300, 640, 9216), (1100, 320, 16384), (1, 256, 32768)])
+@pytest.mark.parametrize("M,N,K", [(16, 64, 16384), (300, 640, 9216), (1100, 320, 16384), (1, 256, 32768), (2300, 1300, 4104),
+                                   (2300, 1031, 8200), (2048, 2048, 12296), (2500, 1100, 16384)])
 def test_float32_output_of_long_bf16_sums(M, N, K):
     """A float32 output of bf16 operands keeps float32's worth: the tensor core
     rounds its running sum toward zero, at most 2^-23 a step of 16, so a chain

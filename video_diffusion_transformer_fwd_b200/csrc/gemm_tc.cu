@@ -94,7 +94,8 @@ struct TcParams {
   int *watchdog;
   const void *ss_hi; int *dbg;            // debug bounds checks: end of ss
   LinEpilogue lin;                        // EPI_LINEAR
-  int bn, stages; uint32_t idesc;         // EPI_LINEAR: columns of a pair tile
+  // EPI_LINEAR: columns of a pair tile, accumulators of a tile and K steps of each
+  int bn, stages, nacc, chunk; uint32_t idesc;
 };
 // stages of wan_linear's ring for tiles of bn columns
 constexpr int lin_stages(int bn) {
@@ -229,6 +230,7 @@ struct LinearEpilogue {
   // returns when all tiles are done, or a wait gave up
   __device__ __forceinline__ void run(uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty) {
     const uint32_t free0 = mapa_shared(smem_u32(&tempty[0]), 0), free1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    const int nbuf = p.nacc > 1 ? 1 : G::NACC;
     const bool tma_out = e.vec_out;
     tma_res = e.res && e.vec_res;
     int stores = 0;
@@ -236,7 +238,7 @@ struct LinearEpilogue {
     if (tma_res) ask_next();
     int i = 0;
     for (int t = pair; t < p.num_tiles; t += npairs, ++i) {
-      const int buf = i & 1;
+      const int buf = i % nbuf;
       int m0, n0;
       corner(t, m0, n0);
       const int m = m0 + lane;
@@ -266,15 +268,23 @@ struct LinearEpilogue {
         rs = m < p.M ? e.a_scale[m] : 0.f;
         if (!rows) rs *= e.w_scale[0];
       }
-      const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i >> 1) & 1, abort_flag, p.watchdog, 0x122);
+      const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122);
       if (!__all_sync(0xffffffffu, ready)) break;
       tc_fence_after();
       const int chunks = p.bn / 32;
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + buf * G::BN + c * 32, r);
+        const uint32_t at = tmem_base + ((uint32_t)(q * 32) << 16) + buf * G::BN + c * 32;
+        tmem_ld32(at, r);
         tmem_ld_wait();
+        for (int a = 1; a < p.nacc; ++a) {
+          uint32_t r2[32];
+          tmem_ld32(at + a * p.bn, r2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
+        }
         if (c + 2 >= chunks) {
           tc_fence_before();
           __syncwarp();
@@ -354,6 +364,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int BN = LIN ? p.bn : G::BN, STAGES = LIN ? p.stages : G::STAGES;
   const int B_BYTES = LIN ? p.bn / 2 * 128 : G::B_BYTES, STAGE_BYTES = A_BYTES + B_BYTES;
   constexpr int NACC = G::NACC, NSTG = G::NSTG;
+  const int nbuf = LIN && p.nacc > 1 ? 1 : NACC;         // tiles in TMEM
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sA = smem;
@@ -460,14 +471,17 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int i = 0;
       bool ok = true;
       for (int t = pair; t < p.num_tiles && ok; t += npairs, ++i) {
-        const int buf = i % NACC;
-        const uint32_t acc_phase = (i / NACC) & 1;
+        const int buf = i % nbuf;
+        const uint32_t acc_phase = (i / nbuf) & 1;
         if (!mbar_wait(smem_u32(&tempty[buf]), acc_phase ^ 1, abort_flag, p.watchdog, 0x111)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * G::BN;
-        for (int kb = 0; kb < p.num_k; ++kb) {
+        for (int kb = 0, acc = 0, in_chunk = 0; kb < p.num_k; ++kb) {
           if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112)) { ok = false; break; }
           tc_fence_after();
+          // wan_linear may spread K over several accumulators
+          const uint32_t da = LIN ? d + acc * BN : d;
+          const int first = LIN ? in_chunk : kb;
           const uint64_t a0 = desc_kmajor_sw128(smem_u32(sA + stage * A_BYTES));
           const uint64_t b0 = desc_kmajor_sw128(smem_u32(sB + stage * B_BYTES));
           // 4 MMAs of 32 bytes of K per stage (16 bf16 or 32 e4m3 each):
@@ -480,14 +494,15 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk) {
                 if (F8)
-                  mma_ss_pair_f8(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (kb | kk) != 0);
+                  mma_ss_pair_f8(da + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (first | kk) != 0);
                 else
-                  mma_ss_pair(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (kb | kk) != 0);
+                  mma_ss_pair(da + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (first | kk) != 0);
               }
             }
             tc_commit_both(smem_u32(&empty[stage]));
           }
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          if (LIN && ++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
         }
         if (ok && elect_one()) tc_commit_both(smem_u32(&tfull[buf]));
       }
@@ -804,8 +819,10 @@ int launch_epi(int epi, const CUtensorMap &ta, const CUtensorMap *tb, const CUte
 
 // wan_linear on CTA pairs: the same products with wan_linear's epilogue, in
 // tiles of 256 rows and bn columns. K may end inside a step and N inside a tile
-// (the TMA unit fills zeros).
-int gemm_tc_linear(const LinArgs &g, int bn, cudaStream_t s) {
+// (the TMA unit fills zeros). With nacc > 1 a tile's K is spread over nacc
+// accumulators (nacc bn <= 512), and its epilogue does not overlap the next
+// tile's products.
+int gemm_tc_linear(const LinArgs &g, int bn, int nacc, cudaStream_t s) {
   CUtensorMap ta, tb[3], tx;
   const int bk = g.fp8 ? BK8 : BK;
   int rc;
@@ -834,6 +851,8 @@ int gemm_tc_linear(const LinArgs &g, int bn, cudaStream_t s) {
   if ((long long)p.num_m * p.num_n > 0x3fffffff) return set_error(WAN_EINVAL, "linear: M=%d N=%d too large", g.M, g.N);
   p.num_tiles = p.num_m * p.num_n;
   p.num_k = (g.K + bk - 1) / bk;
+  p.nacc = nacc;
+  p.chunk = (p.num_k + nacc - 1) / nacc;
   p.L = p.H = p.W = 1; p.head_dim = 128; p.rows_per_gate = 1;
   p.watchdog = watchdog_ptr();
   p.dbg = dbg_word();

@@ -350,13 +350,16 @@ long long ctas_per_sm(const LinArgs &g, const Cut &c) {
   const int sms = c.split > 1 ? SMS * 7 / 8 : SMS;
   return (ctas_of(g, c) + sms - 1) / sms;
 }
-// Accumulators of a CTA. bf16 products are accumulated by the tensor core with
-// a rounding toward zero that grows with the number of steps (relative 1.1e-9
-// K, measured against 64 bits): harmless under a bf16 output, but a float32
-// output gets a new accumulator every 64 steps (4096 of K), added in float32.
+// Accumulators for nkb steps of K, at most `most`. bf16 products are
+// accumulated by the tensor core with a rounding toward zero that grows with
+// the number of steps (relative 1.1e-9 K, measured against 64 bits): harmless
+// under a bf16 output, but a float32 output gets a new accumulator every 64
+// steps (4096 of K), added in float32.
+int chains(const LinArgs &g, int nkb, int most) {
+  return !g.fp8 && g.out_f32 ? std::max(1, std::min((nkb + 63) / 64, most)) : 1;
+}
 int accumulators_of(const LinArgs &g, int num_k, const Cut &c) {
-  const int nkb = (num_k + c.split - 1) / c.split;
-  return !g.fp8 && g.out_f32 ? std::max(1, std::min((nkb + 63) / 64, 512 / c.mt)) : 1;
+  return chains(g, (num_k + c.split - 1) / c.split, 512 / c.mt);
 }
 // TMEM columns. CTAs of a cluster wait for one another, so none may wait for
 // TMEM that a CTA of another cluster holds on the same SM. So a CTA takes 128
@@ -404,25 +407,28 @@ double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   auto ingest = [&](double bytes, double readers) { return bytes * (1.0 / hbm / readers + (1.0 - 1.0 / readers) / 55.0); };
   const double step = ingest(W_BYTES, ntm) + ingest((double)std::min(c.mt, g.M) * ROW_BYTES, ntn);
   const double dram = ((double)g.M + g.N) * g.K * (g.fp8 ? 1 : 2) / 3400.0;
-  return 9500.0 + 10.0 * c.mt * per_sm + (c.split > 1 ? 100.0 * c.split : 0.0) +
+  return 8500.0 + 45.0 * c.mt + 10.0 * c.mt * (per_sm - 1.0) + (c.split > 1 ? 600.0 + 100.0 * c.split : 0.0) +
          4000.0 * (ceil(per_sm / resident(g, num_k, c)) - 1.0) + std::max(per_sm * nkb * step, dram);
 }
+// A pair tile's accumulators: the most that leave it 128 of TMEM's 512 columns
+int pair_chains(const LinArgs &g, int num_k) { return chains(g, num_k, 4); }
 // The same of the pair kernel: tiles of 256 x bn in rounds of 74 pairs. A step
-// of K takes what its operands' way through shared memory takes (written,
-// read, and B read for the other CTA of the pair too, at 128 bytes a cycle: 640
-// cycles at bn = 256, 512 of them the products'), a tile no less than its
-// epilogue (9000 cycles at bn = 256; 20000 where the rows of out or residual
-// are out of the TMA unit's reach); the last one is in the open.
+// of K takes its products (2 bn cycles) or its operands' way onto the SM (60
+// bytes a cycle: measured 560 cycles at bn = 256, 444 at 160), a tile no less
+// than its epilogue (9000 cycles at bn = 256; 20000 where the rows of out or
+// residual are out of the TMA unit's reach); the last one is in the open.
 double pair_cost(const LinArgs &g, int num_k, int bn) {
   const double tiles = ceil(g.M / 256.0) * ceil(g.N / (double)bn);
   const LinEpilogue e = lin_epilogue(g);
   const double epi = (e.vec_out && e.vec_res ? 9000.0 : 20000.0) * bn / 256.0;
-  return 8000.0 + epi + ceil(tiles / 74.0) * std::max(num_k * (256.0 + 1.5 * bn), epi);
+  const double step = std::max(2.0 * bn, (W_BYTES + 64.0 * bn) / 60.0), rounds = ceil(tiles / 74.0);
+  if (pair_chains(g, num_k) > 1) return 8000.0 + rounds * (num_k * step + epi);
+  return 8000.0 + epi + rounds * std::max(num_k * step, epi);
 }
 
 // The kernel of a call: pair_bn != 0 for the pair kernel, else the plan.
 struct Choice {
-  int pair_bn;
+  int pair_bn, pair_nacc;
   Plan plan;
 };
 Choice choose(const LinArgs &g) {
@@ -439,16 +445,13 @@ Choice choose(const LinArgs &g) {
       if (!cut.mt || cost < best) { best = cost; cut = c; }
     }
   }
-  // the pair kernel keeps one accumulator per tile: not for float32 outputs of
-  // bf16 sums longer than 4096 (accumulators_of)
   int bn = 0;
-  if (!cut.mt || g.fp8 || !g.out_f32 || g.K <= 4096) {
-    for (int n = 256; n >= 96; n -= 32) {
-      const double cost = pair_cost(g, num_k, n);
-      if ((!cut.mt && !bn) || cost < best) { best = cost; bn = n; }
-    }
+  for (int n = 256; n >= 96; n -= 32) {
+    if (n * pair_chains(g, num_k) > 512) continue;
+    const double cost = pair_cost(g, num_k, n);
+    if ((!cut.mt && !bn) || cost < best) { best = cost; bn = n; }
   }
-  return bn ? Choice{bn, Plan{}} : Choice{0, make_plan(g, num_k, cut)};
+  return bn ? Choice{bn, pair_chains(g, num_k), Plan{}} : Choice{0, 0, make_plan(g, num_k, cut)};
 }
 
 template <bool F8>
@@ -514,7 +517,7 @@ int launch_linear(const LinArgs &g, cudaStream_t s) {
   if (k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
     k = Known{g.M, g.N, g.K, kind, choose(g)};
   }
-  return k.choice.pair_bn ? gemm_tc_linear(g, k.choice.pair_bn, s) : launch_plan(g, k.choice.plan, s);
+  return k.choice.pair_bn ? gemm_tc_linear(g, k.choice.pair_bn, k.choice.pair_nacc, s) : launch_plan(g, k.choice.plan, s);
 }
 
 }  // namespace wan

@@ -16,7 +16,7 @@ struct LinArgs {
   void *out; int out_f32; long long ldo;
 };
 int launch_linear(const LinArgs &g, cudaStream_t s);
-int gemm_tc_linear(const LinArgs &g, int bn, cudaStream_t s);   // CTA pairs (gemm_tc.cu)
+int gemm_tc_linear(const LinArgs &g, int bn, int nacc, cudaStream_t s);   // CTA pairs (gemm_tc.cu)
 
 struct LinEpilogue {
   const float *a_scale, *w_scale; int w_scale_rows;
