@@ -4,7 +4,7 @@
 //
 // on bf16 operands or e4m3 codes. This file holds the kernel for few rows: the
 // WEIGHT rows are the 128-row operand of tcgen05.mma and the tokens its
-// columns (N = 16 .. 256), so a call with one token pads it to 16 columns and
+// columns (N = 16 .. 128), so a call with one token pads it to 16 columns and
 // not to a 128-row tile. What bounds it is the stream of weights from HBM:
 // each CTA keeps a ring of TMA stages (128 weight rows x 128 bytes of K, and
 // the same K of its tokens) in flight, and K is split over the CTAs of a
@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <mutex>
 
 namespace wan {
 
@@ -343,30 +344,39 @@ int recv_bytes(const Cut &c) { return c.split > 1 ? (c.mt / GROUP + c.split - 1)
 long long ctas_of(const LinArgs &g, const Cut &c) {
   return (long long)((g.N + WROWS - 1) / WROWS) * c.split * ((g.M + c.mt - 1) / c.mt);
 }
-// CTAs of the grid that share an SM. Clusters do not fill a GPC's SMs to the
-// last one: 1 x 5120 x 5120 in 40 clusters of 7 took 20 us with room for two
-// CTAs per SM (280 of 296), 14 us in clusters of 6 or 8.
-long long ctas_per_sm(const LinArgs &g, const Cut &c) {
-  const int sms = c.split > 1 ? SMS * 7 / 8 : SMS;
-  return (ctas_of(g, c) + sms - 1) / sms;
+// Clusters of `split` CTAs that the card holds at once with one CTA to an SM: a
+// GPC's SMs are not filled to the last one (16 clusters of 8 took two waves, 22
+// of 6 one), so the runtime is asked, once for a device. It does not count
+// several CTAs of a kernel to an SM; r of them make room for r times as many
+// (40 clusters of 6 fit in two to an SM, 40 of 7 did not).
+constexpr int MAX_SPLIT = 8, MAX_RESIDENT = 3;
+struct Capacity {
+  int clusters[MAX_SPLIT + 1];
+};
+const Capacity &capacity();
+// CTAs of the grid that share an SM
+int ctas_per_sm(const LinArgs &g, const Cut &c) {
+  const long long clusters = ctas_of(g, c) / c.split;
+  const int room = capacity().clusters[c.split];
+  return (int)((clusters + room - 1) / room);
 }
-// Accumulators for nkb steps of K, at most `most`. bf16 products are
-// accumulated by the tensor core with a rounding toward zero that grows with
-// the number of steps (relative 1.1e-9 K, measured against 64 bits): harmless
-// under a bf16 output, but a float32 output gets a new accumulator every 64
-// steps (4096 of K), added in float32.
-int chains(const LinArgs &g, int nkb, int most) {
-  return !g.fp8 && g.out_f32 ? std::max(1, std::min((nkb + 63) / 64, most)) : 1;
-}
+// TMEM columns that a CTA has without asking for more than its share
+constexpr int TMEM_SHARE = 128;
+// Accumulators of a CTA. bf16 products are accumulated by the tensor core with
+// a rounding toward zero that grows with the number of steps (relative 1.1e-9
+// K, measured against 64 bits): harmless under a bf16 output, but a float32
+// output gets a new accumulator every 16 steps (1024 of K) as far as the share
+// goes, and every 32 steps beyond it; they are added in float32.
 int accumulators_of(const LinArgs &g, int num_k, const Cut &c) {
-  return chains(g, (num_k + c.split - 1) / c.split, 512 / c.mt);
+  if (g.fp8 || !g.out_f32) return 1;
+  const int nkb = (num_k + c.split - 1) / c.split;
+  return std::max(std::max(1, std::min((nkb + 15) / 16, TMEM_SHARE / c.mt)), std::min((nkb + 31) / 32, 512 / c.mt));
 }
 // TMEM columns. CTAs of a cluster wait for one another, so none may wait for
 // TMEM that a CTA of another cluster holds on the same SM. So a CTA takes 128
 // columns, in one size for no gaps between them, and at least a quarter of the
 // SM's shared memory with them, or more columns, and then so much shared memory
 // that no other one fits beside it.
-constexpr int TMEM_SHARE = 128;
 constexpr int SMEM_SHARE = SM_SMEM / 4 - CTA_EXTRA, SMEM_ALONE = SM_SMEM - SM_SMEM / 4;
 int columns_of(const LinArgs &g, int num_k, const Cut &c) {
   int cols = TMEM_SHARE;
@@ -377,7 +387,7 @@ int columns_of(const LinArgs &g, int num_k, const Cut &c) {
 int resident(const LinArgs &g, int num_k, const Cut &c) {
   if (columns_of(g, num_k, c) > TMEM_SHARE) return 1;
   const int fit = SM_SMEM / (3 * stage_of(c) + 1024 + CTA_EXTRA);
-  return (int)std::min<long long>(std::min(fit, 3), ctas_per_sm(g, c));
+  return std::min(std::min(fit, MAX_RESIDENT), ctas_per_sm(g, c));
 }
 
 Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
@@ -395,35 +405,46 @@ Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
 }
 
 // Time of a cut in SM cycles, to compare cuts and kernels by: a start and an
-// end, what an SM takes in for its CTAs, and a new start for every further wave.
-// Measured: an SM takes in 28 bytes a cycle from HBM (22 with one CTA) and 55
-// from L2 (an operand comes from HBM for the first tile that reads it), and the
-// card 3400 from HBM.
+// end, the sums' way through the cluster, what an SM takes in for its CTAs, and
+// a new start and epilogue for every further wave. Measured: an SM takes in 28
+// bytes a cycle from HBM (22 with one CTA) and 55 from L2 (an operand comes from
+// HBM for the first tile that reads it), and the card 3400 from HBM; SM and CTAs
+// need 400 cycles for a step of K at least; a token costs the epilogue 45, 70
+// with a residual. The cut or pair tile taken by these two costs was 2 to 6%
+// slower in the mean than the best of all, over four sets of 40 random sizes.
 double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + c.mt - 1) / c.mt;
-  const double per_sm = (double)ctas_per_sm(g, c);
+  const double per_sm = ctas_per_sm(g, c);
   const int nkb = (num_k + c.split - 1) / c.split;
   const double hbm = per_sm > 1.0 ? 28.0 : 22.0;
   auto ingest = [&](double bytes, double readers) { return bytes * (1.0 / hbm / readers + (1.0 - 1.0 / readers) / 55.0); };
   const double step = ingest(W_BYTES, ntm) + ingest((double)std::min(c.mt, g.M) * ROW_BYTES, ntn);
   const double dram = ((double)g.M + g.N) * g.K * (g.fp8 ? 1 : 2) / 3400.0;
-  return 8500.0 + 45.0 * c.mt + 10.0 * c.mt * (per_sm - 1.0) + (c.split > 1 ? 600.0 + 100.0 * c.split : 0.0) +
-         4000.0 * (ceil(per_sm / resident(g, num_k, c)) - 1.0) + std::max(per_sm * nkb * step, dram);
+  const double waves = ceil(per_sm / resident(g, num_k, c)), finish = (g.res ? 70.0 : 45.0) * c.mt / (c.split > 1 ? 2.0 : 1.0);
+  return 8500.0 + waves * finish + 10.0 * c.mt * (per_sm - 1.0) + (c.split > 1 ? 2200.0 + 100.0 * c.split : 0.0) +
+         4000.0 * (waves - 1.0) + std::max(std::max(per_sm * step, 400.0) * nkb, dram);
 }
-// A pair tile's accumulators: the most that leave it 128 of TMEM's 512 columns
-int pair_chains(const LinArgs &g, int num_k) { return chains(g, num_k, 4); }
+// A pair tile's accumulators, every 32 steps (accumulators_of) while they leave
+// it 128 of TMEM's 512 columns
+int pair_chains(const LinArgs &g, int num_k) {
+  return g.fp8 || !g.out_f32 ? 1 : std::max(1, std::min((num_k + 31) / 32, 4));
+}
 // The same of the pair kernel: tiles of 256 x bn in rounds of 74 pairs. A step
 // of K takes its products (2 bn cycles) or its operands' way onto the SM (60
-// bytes a cycle: measured 560 cycles at bn = 256, 444 at 160), a tile no less
-// than its epilogue (9000 cycles at bn = 256; 20000 where the rows of out or
-// residual are out of the TMA unit's reach); the last one is in the open.
+// bytes a cycle, 28 from HBM: measured 560 cycles at bn = 256, 444 at 160), a
+// tile no less than its epilogue (9000 cycles at bn = 256, more with a residual,
+// 20000 where the rows of out or residual are out of the TMA unit's reach); the
+// last one is in the open, and with several accumulators to a tile each is.
 double pair_cost(const LinArgs &g, int num_k, int bn) {
   const double tiles = ceil(g.M / 256.0) * ceil(g.N / (double)bn);
   const LinEpilogue e = lin_epilogue(g);
-  const double epi = (e.vec_out && e.vec_res ? 9000.0 : 20000.0) * bn / 256.0;
-  const double step = std::max(2.0 * bn, (W_BYTES + 64.0 * bn) / 60.0), rounds = ceil(tiles / 74.0);
-  if (pair_chains(g, num_k) > 1) return 8000.0 + rounds * (num_k * step + epi);
-  return 8000.0 + epi + rounds * std::max(num_k * step, epi);
+  const double epi = 3000.0 + (e.vec_out && e.vec_res ? (g.res ? 8500.0 : 6000.0) : 17000.0) * bn / 256.0;
+  // bytes of a step that no other tile has brought into L2
+  const double cold = 64.0 * bn / ceil(g.M / 256.0) + W_BYTES * std::min(1.0, g.M / 256.0) / ceil(g.N / (double)bn);
+  const double step = std::max(2.0 * bn, cold / 28.0 + std::max(0.0, W_BYTES + 64.0 * bn - cold) / 60.0);
+  const double rounds = ceil(tiles / 74.0);
+  const double again = pair_chains(g, num_k) > 1 ? num_k * step + epi : std::max(num_k * step, epi);
+  return 10000.0 + num_k * step + epi + (rounds - 1.0) * again;
 }
 
 // The kernel of a call: pair_bn != 0 for the pair kernel, else the plan.
@@ -439,7 +460,7 @@ Choice choose(const LinArgs &g) {
     if (want > 16 && want - 16 >= g.M) break;
     const int tiles = (g.M + want - 1) / want, mt = round_up((g.M + tiles - 1) / tiles, 16);
     if (tiles > 65535) continue;
-    for (int split = 1; split <= std::min(8, num_k); ++split) {
+    for (int split = 1; split <= std::min(MAX_SPLIT, num_k); ++split) {
       const Cut c = {mt, split};
       const double cost = split_cost(g, num_k, c);
       if (!cut.mt || cost < best) { best = cost; cut = c; }
@@ -455,7 +476,7 @@ Choice choose(const LinArgs &g) {
 }
 
 template <bool F8>
-int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
+int set_attributes() {
   static std::atomic<uint64_t> ready{0};       // devices whose attributes are set
   int dev = 0;
   WAN_TRY_CUDA(cudaGetDevice(&dev), "linear device");
@@ -466,6 +487,43 @@ int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
                  "linear smem carveout");
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
   }
+  return WAN_OK;
+}
+
+// Where the runtime gives no answer, 7/8 of the SMs count.
+const Capacity &capacity() {
+  static Capacity known[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  std::call_once(once[dev], [&] {
+    const bool ask = set_attributes<false>() == WAN_OK;
+    for (int split = 1; split <= MAX_SPLIT; ++split) {
+      int n = SMS / split;
+      if (split > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = split; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(split * SMS), 1, 1);
+        cfg.blockDim = dim3(THREADS, 1, 1);
+        cfg.dynamicSmemBytes = SMEM_MAX;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int got = 0;
+        if (ask && cudaOccupancyMaxActiveClusters(&got, linear_split_kernel<false>, &cfg) == cudaSuccess && got > 0) n = got;
+        else n = n * 7 / 8;
+      }
+      known[dev].clusters[split] = n;
+    }
+    cudaGetLastError();                        // a refused question is no error of the call
+  });
+  return known[dev];
+}
+
+template <bool F8>
+int launch(const LinArgs &g, const Plan &pl, cudaStream_t s) {
+  if (const int bad = set_attributes<F8>()) return bad;
   CUtensorMap tw, ta;
   int rc;
   if (F8) {
