@@ -411,7 +411,7 @@ Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
 // HBM for the first tile that reads it), and the card 3400 from HBM; SM and CTAs
 // need 400 cycles for a step of K at least; a token costs the epilogue 45, 70
 // with a residual. The cut or pair tile taken by these two costs was 2 to 6%
-// slower in the mean than the best of all, over four sets of 40 random sizes.
+// slower in the mean than the best of all, over four sets of 26 random sizes.
 double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + c.mt - 1) / c.mt;
   const double per_sm = ctas_per_sm(g, c);
