@@ -1,0 +1,120 @@
+"""wan_linear under calls that its documentation allows beside the plain one:
+after other calls of the same sizes, from several threads, on rows more than
+2^31 elements apart, captured at sizes that never ran, and on a device where an
+earlier wait gave up."""
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+import torch
+
+from video_diffusion_transformer_fwd_b200 import wan
+
+from test_gpu_linear import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    wan.load()
+
+
+def new_thread(call):
+    """call() on a thread that has made no call before."""
+    with ThreadPoolExecutor(1) as pool:
+        return pool.submit(call).result()
+
+
+@pytest.mark.parametrize("M", [5, 2500])
+def test_first_call_of_a_thread(M):
+    """A thread that has made no CUDA call of its own."""
+    c = Case(M, 512, 256, f8=True, res="f32", out="f32")
+    out = torch.empty_like(c.r)
+    want = c.run()
+    torch.cuda.synchronize()
+    s = torch.cuda.current_stream()
+    new_thread(lambda: c.run(out=out, stream=s))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+# float32 outputs show every change in the order of a sum
+@pytest.mark.parametrize("M,N,K", [(20, 700, 4096), (100, 1000, 2048), (100, 1500, 4096), (150, 900, 3000), (260, 1100, 1536),
+                                   (300, 640, 2560), (600, 512, 4096), (1100, 320, 5120), (1500, 512, 2048)])
+@pytest.mark.parametrize("f8", [False, True])
+def test_results_do_not_depend_on_the_calls_before(M, N, K, f8):
+    K = K // 16 * 16
+    c = Case(M, N, K, f8, res="f32", out="f32")
+
+    def both(*residuals):
+        return [c.run(residual=r) for r in residuals]
+
+    first, second = new_thread(lambda: both(c.r, None)), new_thread(lambda: both(None, c.r))
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], second[1]) and torch.equal(first[1], second[0])
+
+
+def test_four_threads_at_once():
+    cs = [Case(M, N, K, f8, "gelu_tanh", res="bf16", out="bf16", seed=M)
+          for M, N, K, f8 in ((1, 1536, 4096, False), (24, 2000, 1024, True), (300, 1003, 1000, False), (2500, 512, 768, True))]
+    want = [c.run() for c in cs]
+    torch.cuda.synchronize()
+
+    def many(c):
+        st = torch.cuda.Stream()
+        outs = [torch.empty_like(c.r) for _ in range(30)]
+        for o in outs:
+            c.run(out=o, stream=st)
+        st.synchronize()
+        return outs
+
+    with ThreadPoolExecutor(4) as pool:
+        got = list(pool.map(many, cs))
+    assert all(torch.equal(o, w) for outs, w in zip(got, want) for o in outs)
+
+
+@pytest.mark.parametrize("M,N,ld", [(40, 200, 1 << 26), (40, 203, (1 << 26) + 3), (2304, 264, 1 << 20)])
+def test_rows_pass_32_bits(M, N, ld):
+    """Few rows and CTA pairs, an output and a residual in place whose last rows
+    lie more than 2^31 elements behind the first."""
+    c = Case(M, N, 256, res="bf16")
+    flat = torch.zeros((M - 1) * ld + N, device="cuda", dtype=torch.bfloat16)
+    out = flat.as_strided((M, N), (ld, 1))
+    out.copy_(c.r)
+    assert out.stride(0) * (M - 1) > 2 ** 31
+    c.run(residual=out, out=out)
+    c.check(out.contiguous())
+    assert int(flat.count_nonzero()) <= M * N
+    assert wan.device_status() == wan.WAN_OK
+
+
+def test_capture_at_new_sizes():
+    """Sizes that no call had before the capture."""
+    cs = [Case(M, N, K, f8, "silu", res="f32", out="f32") for M, N, K, f8 in
+          ((3, 1111, 2056, False), (77, 1311, 2064, True), (1111, 515, 528, False), (3333, 777, 1040, True))]
+    outs = [torch.zeros(c.r.shape, device="cuda") for c in cs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, o in zip(cs, outs):
+            c.run(out=o)
+    graph.replay()
+    torch.cuda.synchronize()
+    for c, o in zip(cs, outs):
+        c.check(o)
+
+
+@pytest.mark.parametrize("M,N,K,f8", [(1, 1536, 8192, False), (37, 600, 8192, True), (90, 520, 6400, False), (2304, 512, 640, True)])
+def test_after_a_wait_that_gave_up(M, N, K, f8):
+    """Launches on a device whose status is set end at once, the context stays
+    usable, and the same call is right once the status has been read."""
+    s = torch.cuda.current_stream().cuda_stream
+    c = Case(M, N, K, f8, res="f32", out="f32")
+    wan.check(wan.wan_selftest_watchdog(s))
+    for _ in range(3):
+        c.run()
+    assert wan.wan_device_status(s) == wan.WAN_ETIMEOUT
+    assert wan.wan_device_status(s) == wan.WAN_OK
+    c.check(c.run())
+    assert wan.device_status() == wan.WAN_OK

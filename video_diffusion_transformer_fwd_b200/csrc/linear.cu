@@ -276,25 +276,26 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     if (split > 1) {
       if (!early) cluster_arrive();
       cluster_wait();
-      if (ok) {
-        for (int c = 0; c < rows; c += 16) {
-          float v[16];
-          accumulators(taddr, c, naccs, p.mt, v);
+      // A CTA that gave up sends zeros, and waits for the others' sums like the
+      // rest: nothing is on its way to a CTA that has ended.
+      for (int c = 0; c < rows; c += 16) {
+        float v[16] = {};
+        if (ok) accumulators(taddr, c, naccs, p.mt, v);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int g = c / GROUP + k, owner = g % split;
-            if (g >= groups) break;
-            const float4 s4 = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            uint8_t *at = recv + (rank * most + g / split) * GROUP_BYTES;
-            if (owner == rank) *reinterpret_cast<float4 *>(at) = s4;
-            else st_async_cluster(mapa_shared(smem_u32(at), owner), s4, mapa_shared(smem_u32(&arrived), owner));
-          }
+        for (int k = 0; k < 4; ++k) {
+          const int g = c / GROUP + k, owner = g % split;
+          if (g >= groups) break;
+          const float4 s4 = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          uint8_t *at = recv + (rank * most + g / split) * GROUP_BYTES;
+          if (owner == rank) *reinterpret_cast<float4 *>(at) = s4;
+          else st_async_cluster(mapa_shared(smem_u32(at), owner), s4, mapa_shared(smem_u32(&arrived), owner));
         }
       }
       cluster_arrive();                      // nothing more leaves this warp
-      if (ok && mine > 0) {
-        ok = mbar_wait_cluster(smem_u32(&arrived), 0, &abort_flag, p.watchdog, 0x222);
-        ok = __all_sync(0xffffffffu, ok);
+      if (mine > 0) {
+        int never = 0;
+        const bool all = mbar_wait_cluster(smem_u32(&arrived), 0, &never, p.watchdog, 0x222);
+        ok = __all_sync(0xffffffffu, ok && all);
       }
     }
     if (ok) {
@@ -562,14 +563,15 @@ int launch_plan(const LinArgs &g, const Plan &pl, cudaStream_t s) {
 }  // namespace
 
 int launch_linear(const LinArgs &g, cudaStream_t s) {
-  // the choice costs a few microseconds of the host: the last ones are kept, by sizes and types
+  // the choice costs a few microseconds of the host: the last ones are kept, by
+  // all that it is made from (sizes, types, the rows' alignment, a residual)
   struct Known {
     int M, N, K, kind;
     Choice choice;
   };
   thread_local Known known[32] = {};
   const LinEpilogue e = lin_epilogue(g);
-  const int kind = 1 | (g.fp8 ? 2 : 0) | (g.out_f32 ? 4 : 0) | (e.vec_out && e.vec_res ? 8 : 0);
+  const int kind = 1 | (g.fp8 ? 2 : 0) | (g.out_f32 ? 4 : 0) | (e.vec_out && e.vec_res ? 8 : 0) | (g.res ? 16 : 0);
   const unsigned h = ((unsigned)g.M * 2654435761u ^ (unsigned)g.N * 40503u ^ (unsigned)g.K * 65599u ^ (unsigned)kind) >> 3;
   Known &k = known[h % 32];
   if (k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
