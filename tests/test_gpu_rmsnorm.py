@@ -64,7 +64,7 @@ def check(x, r, g, out, y, scale, h, eps=EPS):
 # one thread to several per row, one warp, one CTA of every register depth; the
 # same for widths that are not multiples of 8
 WIDTHS = [8, 16, 64, 72, 128, 136, 256, 264, 512, 520, 1536, 2048, 2056, 4096, 5120, 8192, 8200, 13824, 16384]
-RAGGED = [1, 3, 7, 9, 31, 33, 57, 58, 127, 129, 500, 507, 1037, 2047, 2049, 7031, 16366, 16370, 16371, 16383]
+RAGGED = [1, 3, 7, 9, 31, 33, 57, 58, 127, 129, 500, 507, 513, 603, 754, 755, 771, 1037, 2047, 2049, 7031, 16366, 16370, 16371, 16383]
 
 
 @pytest.mark.parametrize("D", WIDTHS + RAGGED)

@@ -24,8 +24,13 @@
 //   rmsnorm_ragged_kernel  strides that do not agree: a row comes in and leaves
 //                          in whole 16-byte pieces of memory through shared
 //                          memory, where its elements are picked at their own
-//                          offsets (2.5 times the time of the other kernel at
-//                          12000 x 3163).
+//                          offsets (12000 x 3163 bf16: 82 us, 42 where the
+//                          strides agree).
+// Measured: 32760 x 5120 bf16 onto a float32 stream and into codes 262 us (7.0
+// TB/s), 7800 x 1536 of the same 21.8 (6.0), 93600 x 128 bf16 10.6 (4.5), 2011 x
+// 1037 7.4 (2.8), one row of 5120 2.4 us, which is a launch. Short calls are
+// bound by the launch and one trip to memory; dense rows of odd width by the
+// instructions that pick their elements.
 #include "common.cuh"
 #include "e4m3.cuh"
 
@@ -106,6 +111,47 @@ __device__ __forceinline__ void store8_codes(uint8_t *p, const float (&v)[8], fl
                                                   quant4(make_float4(v[4], v[5], v[6], v[7]), inv)));
 }
 
+// The gain of elements lo .. lo + 7. Rows that begin off a boundary of 8 (SHIFT)
+// take the three aligned float4 around them and move their elements into place
+// by the row's offset (12000 x 3163 bf16: 43 us, 65 with 8 single loads
+// after the row);
+// the groups at the row's ends, whose three would leave the gain, take single
+// elements.
+template <bool SHIFT> struct Gain8 {
+  float4 p, q, r;
+  __device__ __forceinline__ static int offset(int lo, int D) {
+    return SHIFT && lo >= 0 && lo - (lo & 3) + 12 <= D ? lo & 3 : 0;
+  }
+  __device__ __forceinline__ void load(const float *g, int lo, int D) {
+    if (!SHIFT || (lo >= 0 && lo - (lo & 3) + 12 <= D)) {
+      const float4 *at = reinterpret_cast<const float4 *>(g + (SHIFT ? lo - (lo & 3) : lo));
+      p = __ldg(at);
+      q = __ldg(at + 1);
+      if (SHIFT) r = __ldg(at + 2);
+    } else {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = __ldg(g + min(max(lo + e, 0), D - 1));
+      p = make_float4(w[0], w[1], w[2], w[3]);
+      q = make_float4(w[4], w[5], w[6], w[7]);
+      r = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void apply(float (&v)[8], int lo, int D) const {
+    float w[11] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w, 0.f, 0.f, 0.f};
+    if constexpr (SHIFT) {
+      w[8] = r.x; w[9] = r.y; w[10] = r.z;
+      const int off = offset(lo, D);
+#pragma unroll
+      for (int e = 0; e < 10; ++e) w[e] = off & 1 ? w[e + 1] : w[e];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = off & 2 ? w[e + 2] : w[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= w[e];
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ void store_part(T *row, int lo, int D, const float (&v)[8]) {
 #pragma unroll
@@ -178,6 +224,11 @@ __global__ void __launch_bounds__(TPR ? ROW_CTA : VEC_CTA, !TPR && NV == 4 ? 2 :
   float ss = 0.f, top = 0.f;
   Raw8<XT> xv[NV];
   Raw8<RT> rv[NV];
+  // The gain, which every row reads from the caches, comes with the row where
+  // registers allow (32760 x 5120 onto codes: 263 us, 271 when it was read after
+  // the row; rows of a warp are faster so: 93600 x 128 10.7 us, 12.1 with it).
+  constexpr bool EARLY = TPR == 0 && NV <= 2;
+  Gain8<SHIFT> gv[NV];
   if (live) {
     // all loads of the row before the first use of one
     const XT *xr = static_cast<const XT *>(a.x) + row * a.ldx;
@@ -196,6 +247,11 @@ __global__ void __launch_bounds__(TPR ? ROW_CTA : VEC_CTA, !TPR && NV == 4 ? 2 :
           if constexpr (RES) rv[i].load_part(rr, lo_of(c), D);
         }
       }
+    }
+    if (EARLY && a.g) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (t + i * tpr < nv) gv[i].load(a.g, lo_of(t + i * tpr), D);
     }
     RT *hr = RES && a.h ? static_cast<RT *>(a.h) + row * a.ldh : nullptr;
 #pragma unroll
@@ -226,19 +282,9 @@ __global__ void __launch_bounds__(TPR ? ROW_CTA : VEC_CTA, !TPR && NV == 4 ? 2 :
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-        // The gain stays in the caches: every row reads it. (Shifted rows read
-        // it element by element: a copy in shared memory took 70 for 78 us at
-        // 12000 x 3163 bf16, but 165 for 123 at 4000 x 12345.)
         if (a.g) {
-          if constexpr (SHIFT) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] *= __ldg(a.g + min(max(lo + e, 0), D - 1));
-          } else {
-            const float4 p = __ldg(reinterpret_cast<const float4 *>(a.g) + 2 * c);
-            const float4 q = __ldg(reinterpret_cast<const float4 *>(a.g) + 2 * c + 1);
-            v[i][0] *= p.x; v[i][1] *= p.y; v[i][2] *= p.z; v[i][3] *= p.w;
-            v[i][4] *= q.x; v[i][5] *= q.y; v[i][6] *= q.z; v[i][7] *= q.w;
-          }
+          if (!EARLY) gv[i].load(a.g, lo, D);
+          gv[i].apply(v[i], lo, D);
         }
         if constexpr (CODES) {
 #pragma unroll
@@ -377,8 +423,14 @@ template <typename XT, typename RT, bool RES, typename YT, int NV, int TPR>
 int rms_launch(const RmsArgs &a, RowLayout lay, int threads, cudaStream_t s) {
   const int per = TPR ? threads / TPR : 1;
   const long long grid = ((long long)a.rows + per - 1) / per;
-  if (lay == ROWS_ALIGNED) rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, false><<<(unsigned)grid, threads, 0, s>>>(a);
-  else rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, true><<<(unsigned)grid, threads, 0, s>>>(a);
+  if constexpr (TPR || NV > 1) {               // one group a thread, a CTA to a row: shifted rows only
+    if (lay == ROWS_ALIGNED) {
+      rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, false><<<(unsigned)grid, threads, 0, s>>>(a);
+      WAN_CHECK_LAUNCH("rmsnorm");
+      return WAN_OK;
+    }
+  }
+  rmsnorm_kernel<XT, RT, RES, YT, NV, TPR, true><<<(unsigned)grid, threads, 0, s>>>(a);
   WAN_CHECK_LAUNCH("rmsnorm");
   return WAN_OK;
 }
@@ -395,10 +447,11 @@ int rms_launch_ragged(const RmsArgs &a, int threads, cudaStream_t s) {
   return WAN_OK;
 }
 
-// Groups per thread, measured: a warp or part of one holds up to 64 groups; one
-// group a thread up to 128 (40000 x 768 bf16: 37.9 us, 39.4 with two), then two
-// (7800 x 1536 onto f32: 22.5 us, 24.5 with one), four where two would take
-// more than 512 threads.
+// Groups per thread, measured: a warp or part of one holds up to 64 groups; then
+// two a thread (20000 x 1000 f32: 26.7 us, 28.7 with one; 20000 x 777 shifted
+// bf16 29.4, 33.1), but one for shifted rows of up to 96 groups (20000 x 603
+// onto codes: 32.4 us, 38.7 with two), and four where two would take more than
+// 512 threads.
 template <typename XT, typename RT, bool RES, typename YT>
 int rms_shape(const RmsArgs &a, RowLayout lay, cudaStream_t s) {
   const int n = lay == ROWS_RAGGED ? a.D : (a.D + (lay == ROWS_SHIFTED ? 14 : 0)) / 8;   // groups of any row, at most
@@ -408,7 +461,7 @@ int rms_shape(const RmsArgs &a, RowLayout lay, cudaStream_t s) {
     if (n <= 16) return rms_launch<XT, RT, RES, YT, 1, 16>(a, lay, ROW_CTA, s);
     if (n <= 32) return rms_launch<XT, RT, RES, YT, 1, 32>(a, lay, ROW_CTA, s);
     if (n <= 64) return rms_launch<XT, RT, RES, YT, 2, 32>(a, lay, ROW_CTA, s);
-    if (n <= 128) return rms_launch<XT, RT, RES, YT, 1, 0>(a, lay, threads(1), s);
+    if (n <= 96 && lay == ROWS_SHIFTED) return rms_launch<XT, RT, RES, YT, 1, 0>(a, lay, threads(1), s);
     if (n <= 1024) return rms_launch<XT, RT, RES, YT, 2, 0>(a, lay, threads(2), s);
     return rms_launch<XT, RT, RES, YT, 4, 0>(a, lay, threads(4), s);
   }
