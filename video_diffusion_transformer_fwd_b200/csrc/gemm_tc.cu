@@ -94,8 +94,8 @@ struct TcParams {
   int *watchdog;
   const void *ss_hi; int *dbg;            // debug bounds checks: end of ss
   LinEpilogue lin;                        // EPI_LINEAR
-  // EPI_LINEAR: columns of a pair tile, accumulators of a tile and K steps of each
-  int bn, stages, nacc, chunk; uint32_t idesc;
+  // EPI_LINEAR: columns of a pair tile; parts of K with an accumulator of their own, and steps of each
+  int bn, stages, parts, part_steps; uint32_t idesc;
 };
 // stages of wan_linear's ring for tiles of bn columns
 constexpr int lin_stages(int bn) {
@@ -208,6 +208,26 @@ struct LinearEpilogue {
     return true;
   }
 
+  // a chunk of an accumulator, plus the chunk of the sum at `sum` (0: none)
+  __device__ __forceinline__ void load_chunk(uint32_t at, uint32_t sum, uint32_t (&r)[32]) const {
+    tmem_ld32(at, r);
+    if (sum) {
+      uint32_t x[32];
+      tmem_ld32(sum, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(x[j]) + __uint_as_float(r[j]));
+    } else {
+      tmem_ld_wait();
+    }
+  }
+  // this warp is done with an accumulator
+  __device__ __forceinline__ void give_back(uint32_t free_bar) const {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(free_bar);
+  }
+
   // rows that the TMA unit cannot address: column `lane` of the chunk, row by row
   __device__ __forceinline__ void store_by_columns(const float (&v)[32], int m0, int n) {
     uint8_t *tile = tiles + STG_BYTES;
@@ -218,27 +238,50 @@ struct LinearEpilogue {
     __syncwarp();
     if (n + lane >= p.N) return;
     const int rows = min(32, p.M - m0);
-    const bool res = e.res && !tma_res;
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-      float o = *reinterpret_cast<const float *>(slot(tile, r, lane >> 2) + 4 * (lane & 3));
-      if (res) o += lin_res(e, m0 + r, n + lane);
-      lin_put(e, m0 + r, n + lane, o);
+    // 16 rows at a time, all loads of the residual before the first store (rows
+    // past the end read the last one): one by one behind the choice of the type
+    // each waited for the one before
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+      float o[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[r] = *reinterpret_cast<const float *>(slot(tile, r0 + r, lane >> 2) + 4 * (lane & 3));
+      if (e.res && !tma_res) {
+        const long long at = (long long)(m0 + r0) * e.ldr + n + lane;
+        if (e.res_f32) {
+          const float *x = static_cast<const float *>(e.res) + at;
+          float y[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) y[r] = x[min(r, rows - 1 - r0) * e.ldr];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] += y[r];
+        } else {
+          const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(e.res) + at;
+          __nv_bfloat16 y[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) y[r] = x[min(r, rows - 1 - r0) * e.ldr];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] += __bfloat162float(y[r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (r0 + r < rows) lin_put(e, m0 + r0 + r, n + lane, o[r]);
     }
   }
 
   // returns when all tiles are done, or a wait gave up
   __device__ __forceinline__ void run(uint32_t tmem_base, uint64_t *tfull, uint64_t *tempty) {
     const uint32_t free0 = mapa_shared(smem_u32(&tempty[0]), 0), free1 = mapa_shared(smem_u32(&tempty[1]), 0);
-    const int nbuf = p.nacc > 1 ? 1 : G::NACC;
+    constexpr int nbuf = G::NACC;
+    const int buf_cols = p.parts > 1 ? p.bn : G::BN, chunks = p.bn / 32;
     const bool tma_out = e.vec_out;
     tma_res = e.res && e.vec_res;
     int stores = 0;
     rt = pair; rc = half - 2;
     if (tma_res) ask_next();
     int i = 0;
-    for (int t = pair; t < p.num_tiles; t += npairs, ++i) {
-      const int buf = i % nbuf;
+    for (int t = pair; t < p.num_tiles; t += npairs) {
       int m0, n0;
       corner(t, m0, n0);
       const int m = m0 + lane;
@@ -268,28 +311,36 @@ struct LinearEpilogue {
         rs = m < p.M ? e.a_scale[m] : 0.f;
         if (!rows) rs *= e.w_scale[0];
       }
-      const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122);
-      if (!__all_sync(0xffffffffu, ready)) break;
-      tc_fence_after();
-      const int chunks = p.bn / 32;
+      const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16), sum = lanes + 2 * p.bn;
+      // several parts of K: each into the sum, and both accumulators are free
+      // while the tile is finished from there
+      const bool summed = p.parts > 1;
+      for (int part = 0; summed && part < p.parts; ++part, ++i) {
+        const int buf = i % nbuf;
+        const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122);
+        if (!__all_sync(0xffffffffu, ready)) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = half; c < chunks; c += 2) {
+          uint32_t r[32];
+          load_chunk(lanes + buf * buf_cols + c * 32, part ? sum + c * 32 : 0u, r);
+          tmem_st32(sum + c * 32, r);
+        }
+        tmem_st_wait();
+        give_back(buf ? free1 : free0);
+      }
+      const int buf = i % nbuf;
+      if (!summed) {
+        const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122);
+        if (!__all_sync(0xffffffffu, ready)) return;
+        ++i;
+        tc_fence_after();
+      }
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         uint32_t r[32];
-        const uint32_t at = tmem_base + ((uint32_t)(q * 32) << 16) + buf * G::BN + c * 32;
-        tmem_ld32(at, r);
-        tmem_ld_wait();
-        for (int a = 1; a < p.nacc; ++a) {
-          uint32_t r2[32];
-          tmem_ld32(at + a * p.bn, r2);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
-        }
-        if (c + 2 >= chunks) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(buf ? free1 : free0);
-        }
+        load_chunk((summed ? sum : lanes + buf * buf_cols) + c * 32, 0u, r);
+        if (!summed && c + 2 >= chunks) give_back(buf ? free1 : free0);
         const int n = n0 + c * 32;
         if (m0 >= p.M || n >= p.N) continue;     // warp-uniform
         float v[32];
@@ -364,7 +415,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int BN = LIN ? p.bn : G::BN, STAGES = LIN ? p.stages : G::STAGES;
   const int B_BYTES = LIN ? p.bn / 2 * 128 : G::B_BYTES, STAGE_BYTES = A_BYTES + B_BYTES;
   constexpr int NACC = G::NACC, NSTG = G::NSTG;
-  const int nbuf = LIN && p.nacc > 1 ? 1 : NACC;         // tiles in TMEM
+  // accumulators in TMEM, used in turn; with several parts of K the sum of a tile's parts lies behind both
+  constexpr int nbuf = NACC;
+  const int parts = LIN ? p.parts : 1, buf_cols = LIN && p.parts > 1 ? p.bn : G::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sA = smem;
@@ -470,41 +523,41 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       uint32_t phase = 0;
       int i = 0;
       bool ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs, ++i) {
-        const int buf = i % nbuf;
-        const uint32_t acc_phase = (i / nbuf) & 1;
-        if (!mbar_wait(smem_u32(&tempty[buf]), acc_phase ^ 1, abort_flag, p.watchdog, 0x111)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + buf * G::BN;
-        for (int kb = 0, acc = 0, in_chunk = 0; kb < p.num_k; ++kb) {
-          if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112)) { ok = false; break; }
+      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
+        for (int part = 0; part < parts && ok; ++part, ++i) {
+          const int buf = i % nbuf;
+          const uint32_t acc_phase = (i / nbuf) & 1;
+          if (!mbar_wait(smem_u32(&tempty[buf]), acc_phase ^ 1, abort_flag, p.watchdog, 0x111)) { ok = false; break; }
           tc_fence_after();
-          // wan_linear may spread K over several accumulators
-          const uint32_t da = LIN ? d + acc * BN : d;
-          const int first = LIN ? in_chunk : kb;
-          const uint64_t a0 = desc_kmajor_sw128(smem_u32(sA + stage * A_BYTES));
-          const uint64_t b0 = desc_kmajor_sw128(smem_u32(sB + stage * B_BYTES));
-          // 4 MMAs of 32 bytes of K per stage (16 bf16 or 32 e4m3 each):
-          // the descriptor start address advances 32 bytes (2 in 16-byte units)
-          if (elect_one()) {
+          const uint32_t d = tmem_base + buf * buf_cols;
+          const int kb0 = LIN ? part * p.part_steps : 0, kb1 = LIN ? min(p.num_k, kb0 + p.part_steps) : p.num_k;
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112)) { ok = false; break; }
+            tc_fence_after();
+            const int first = kb - kb0;
+            const uint64_t a0 = desc_kmajor_sw128(smem_u32(sA + stage * A_BYTES));
+            const uint64_t b0 = desc_kmajor_sw128(smem_u32(sB + stage * B_BYTES));
+            // 4 MMAs of 32 bytes of K per stage (16 bf16 or 32 e4m3 each):
+            // the descriptor start address advances 32 bytes (2 in 16-byte units)
+            if (elect_one()) {
 #pragma unroll
-            for (int h = 0; h < G::BN / 256; ++h) {
-              // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
-              const uint64_t bh = b0 + (uint64_t)((h * (B_BYTES / 2)) >> 4);
+              for (int h = 0; h < G::BN / 256; ++h) {
+                // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
+                const uint64_t bh = b0 + (uint64_t)((h * (B_BYTES / 2)) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk) {
-                if (F8)
-                  mma_ss_pair_f8(da + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (first | kk) != 0);
-                else
-                  mma_ss_pair(da + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (first | kk) != 0);
+                for (int kk = 0; kk < BK / 16; ++kk) {
+                  if (F8)
+                    mma_ss_pair_f8(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (first | kk) != 0);
+                  else
+                    mma_ss_pair(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (first | kk) != 0);
+                }
               }
+              tc_commit_both(smem_u32(&empty[stage]));
             }
-            tc_commit_both(smem_u32(&empty[stage]));
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
           }
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
-          if (LIN && ++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
+          if (ok && elect_one()) tc_commit_both(smem_u32(&tfull[buf]));
         }
-        if (ok && elect_one()) tc_commit_both(smem_u32(&tfull[buf]));
       }
     }
     __syncwarp();
@@ -819,10 +872,10 @@ int launch_epi(int epi, const CUtensorMap &ta, const CUtensorMap *tb, const CUte
 
 // wan_linear on CTA pairs: the same products with wan_linear's epilogue, in
 // tiles of 256 rows and bn columns. K may end inside a step and N inside a tile
-// (the TMA unit fills zeros). With nacc > 1 a tile's K is spread over nacc
-// accumulators (nacc bn <= 512), and its epilogue does not overlap the next
-// tile's products.
-int gemm_tc_linear(const LinArgs &g, int bn, int nacc, cudaStream_t s) {
+// (the TMA unit fills zeros). A K in several parts (lin_pair_parts) takes the two
+// accumulators in turn; the epilogue warps add them up, in the order of K, in
+// TMEM columns behind both, so bn <= LIN_PARTS_BN.
+int gemm_tc_linear(const LinArgs &g, int bn, cudaStream_t s) {
   CUtensorMap ta, tb[3], tx;
   const int bk = g.fp8 ? BK8 : BK;
   int rc;
@@ -851,8 +904,9 @@ int gemm_tc_linear(const LinArgs &g, int bn, int nacc, cudaStream_t s) {
   if ((long long)p.num_m * p.num_n > 0x3fffffff) return set_error(WAN_EINVAL, "linear: M=%d N=%d too large", g.M, g.N);
   p.num_tiles = p.num_m * p.num_n;
   p.num_k = (g.K + bk - 1) / bk;
-  p.nacc = nacc;
-  p.chunk = (p.num_k + nacc - 1) / nacc;
+  const int parts = lin_pair_parts(g, p.num_k);
+  p.part_steps = (p.num_k + parts - 1) / parts;
+  p.parts = (p.num_k + p.part_steps - 1) / p.part_steps;
   p.L = p.H = p.W = 1; p.head_dim = 128; p.rows_per_gate = 1;
   p.watchdog = watchdog_ptr();
   p.dbg = dbg_word();

@@ -363,15 +363,11 @@ int ctas_per_sm(const LinArgs &g, const Cut &c) {
 }
 // TMEM columns that a CTA has without asking for more than its share
 constexpr int TMEM_SHARE = 128;
-// Accumulators of a CTA. bf16 products are accumulated by the tensor core with
-// a rounding toward zero that grows with the number of steps (relative 1.1e-9
-// K, measured against 64 bits): harmless under a bf16 output, but a float32
-// output gets a new accumulator every 16 steps (1024 of K) as far as the share
-// goes, and every 32 steps beyond it; they are added in float32.
+// Accumulators of a CTA: one for every part of its K (lin_parts), as many as go
+// into its share of TMEM while a part then stays below 16 steps, else into all of it
 int accumulators_of(const LinArgs &g, int num_k, const Cut &c) {
-  if (g.fp8 || !g.out_f32) return 1;
-  const int nkb = (num_k + c.split - 1) / c.split;
-  return std::max(std::max(1, std::min((nkb + 15) / 16, TMEM_SHARE / c.mt)), std::min((nkb + 31) / 32, 512 / c.mt));
+  const int nkb = (num_k + c.split - 1) / c.split, want = lin_parts(g, nkb), share = TMEM_SHARE / c.mt;
+  return std::min(want, nkb <= 16 * share ? share : 512 / c.mt);
 }
 // TMEM columns. CTAs of a cluster wait for one another, so none may wait for
 // TMEM that a CTA of another cluster holds on the same SM. So a CTA takes 128
@@ -425,17 +421,12 @@ double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   return 8500.0 + waves * finish + 10.0 * c.mt * (per_sm - 1.0) + (c.split > 1 ? 2200.0 + 100.0 * c.split : 0.0) +
          4000.0 * (waves - 1.0) + std::max(std::max(per_sm * step, 400.0) * nkb, dram);
 }
-// A pair tile's accumulators, every 32 steps (accumulators_of) while they leave
-// it 128 of TMEM's 512 columns
-int pair_chains(const LinArgs &g, int num_k) {
-  return g.fp8 || !g.out_f32 ? 1 : std::max(1, std::min((num_k + 31) / 32, 4));
-}
 // The same of the pair kernel: tiles of 256 x bn in rounds of 74 pairs. A step
 // of K takes its products (2 bn cycles) or its operands' way onto the SM (60
 // bytes a cycle, 28 from HBM: measured 560 cycles at bn = 256, 444 at 160), a
 // tile no less than its epilogue (9000 cycles at bn = 256, more with a residual,
 // 20000 where the rows of out or residual are out of the TMA unit's reach); the
-// last one is in the open, and with several accumulators to a tile each is.
+// last one is in the open.
 double pair_cost(const LinArgs &g, int num_k, int bn) {
   const double tiles = ceil(g.M / 256.0) * ceil(g.N / (double)bn);
   const LinEpilogue e = lin_epilogue(g);
@@ -444,13 +435,12 @@ double pair_cost(const LinArgs &g, int num_k, int bn) {
   const double cold = 64.0 * bn / ceil(g.M / 256.0) + W_BYTES * std::min(1.0, g.M / 256.0) / ceil(g.N / (double)bn);
   const double step = std::max(2.0 * bn, cold / 28.0 + std::max(0.0, W_BYTES + 64.0 * bn - cold) / 60.0);
   const double rounds = ceil(tiles / 74.0);
-  const double again = pair_chains(g, num_k) > 1 ? num_k * step + epi : std::max(num_k * step, epi);
-  return 10000.0 + num_k * step + epi + (rounds - 1.0) * again;
+  return 10000.0 + num_k * step + epi + (rounds - 1.0) * std::max(num_k * step, epi);
 }
 
 // The kernel of a call: pair_bn != 0 for the pair kernel, else the plan.
 struct Choice {
-  int pair_bn, pair_nacc;
+  int pair_bn;
   Plan plan;
 };
 Choice choose(const LinArgs &g) {
@@ -468,12 +458,11 @@ Choice choose(const LinArgs &g) {
     }
   }
   int bn = 0;
-  for (int n = 256; n >= 96; n -= 32) {
-    if (n * pair_chains(g, num_k) > 512) continue;
+  for (int n = lin_pair_parts(g, num_k) > 1 ? LIN_PARTS_BN : 256; n >= 96; n -= 32) {
     const double cost = pair_cost(g, num_k, n);
     if ((!cut.mt && !bn) || cost < best) { best = cost; bn = n; }
   }
-  return bn ? Choice{bn, pair_chains(g, num_k), Plan{}} : Choice{0, 0, make_plan(g, num_k, cut)};
+  return bn ? Choice{bn, Plan{}} : Choice{0, make_plan(g, num_k, cut)};
 }
 
 template <bool F8>
@@ -577,7 +566,7 @@ int launch_linear(const LinArgs &g, cudaStream_t s) {
   if (k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
     k = Known{g.M, g.N, g.K, kind, choose(g)};
   }
-  return k.choice.pair_bn ? gemm_tc_linear(g, k.choice.pair_bn, k.choice.pair_nacc, s) : launch_plan(g, k.choice.plan, s);
+  return k.choice.pair_bn ? gemm_tc_linear(g, k.choice.pair_bn, s) : launch_plan(g, k.choice.plan, s);
 }
 
 }  // namespace wan

@@ -16,7 +16,22 @@ struct LinArgs {
   void *out; int out_f32; long long ldo;
 };
 int launch_linear(const LinArgs &g, cudaStream_t s);
-int gemm_tc_linear(const LinArgs &g, int bn, int nacc, cudaStream_t s);   // CTA pairs (gemm_tc.cu)
+int gemm_tc_linear(const LinArgs &g, int bn, cudaStream_t s);   // CTA pairs (gemm_tc.cu)
+
+// The tensor core rounds its running sum of bf16 products toward zero, an error
+// that grows with the number of steps (relative 1.1e-9 K, measured against 64
+// bits). Under a bf16 output that is nothing, but a float32 output gets an
+// accumulator for every 12 steps of 64, and these are added in float32. On CTA
+// pairs only from 33 steps on: one accumulator is off by 2.2e-6 at K = 2048, and
+// parts need narrower tiles (4096 x 4096 x 2048 onto float32: 61 us with one, 72
+// in parts; x 4096: 117 with two of 32 steps, 119 in parts). e4m3 products need
+// none (4.9e-7 at K = 13824).
+constexpr int LIN_PART_STEPS = 12;
+inline int lin_parts(const LinArgs &g, int steps) {
+  return g.fp8 || !g.out_f32 ? 1 : (steps + LIN_PART_STEPS - 1) / LIN_PART_STEPS;
+}
+inline int lin_pair_parts(const LinArgs &g, int steps) { return steps <= 32 ? 1 : lin_parts(g, steps); }
+constexpr int LIN_PARTS_BN = 160;         // widest pair tile with several parts: 3 x 160 of TMEM's 512 columns
 
 struct LinEpilogue {
   const float *a_scale, *w_scale; int w_scale_rows;
@@ -82,14 +97,6 @@ __device__ __forceinline__ void lin_act_row(float (&v)[C], int act) {
   }
 }
 
-__device__ __forceinline__ float lin_res(const LinEpilogue &e, int m, int n) {
-  const long long o = (long long)m * e.ldr + n;
-  return e.res_f32 ? static_cast<const float *>(e.res)[o] : __bfloat162float(static_cast<const __nv_bfloat16 *>(e.res)[o]);
-}
-__device__ __forceinline__ float4 lin_res4(const LinEpilogue &e, int m, int n) {
-  const long long o = (long long)m * e.ldr + n;
-  return e.res_f32 ? load4(static_cast<const float *>(e.res) + o) : load4(static_cast<const __nv_bfloat16 *>(e.res) + o);
-}
 __device__ __forceinline__ void lin_put(const LinEpilogue &e, int m, int n, float v) {
   const long long o = (long long)m * e.ldo + n;
   if (e.out_f32) {
@@ -100,15 +107,4 @@ __device__ __forceinline__ void lin_put(const LinEpilogue &e, int m, int n, floa
     if (WAN_DBG_OK(p, 2, e.out, e.out_hi, e.dbg, WAN_DBG_CODE_BASE + 15)) *p = __float2bfloat16_rn(v);
   }
 }
-__device__ __forceinline__ void lin_put4(const LinEpilogue &e, int m, int n, float4 v) {
-  const long long o = (long long)m * e.ldo + n;
-  if (e.out_f32) {
-    float *p = static_cast<float *>(e.out) + o;
-    if (WAN_DBG_OK(p, 16, e.out, e.out_hi, e.dbg, WAN_DBG_CODE_BASE + 15)) store4(p, v);
-  } else {
-    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(e.out) + o;
-    if (WAN_DBG_OK(p, 8, e.out, e.out_hi, e.dbg, WAN_DBG_CODE_BASE + 15)) store4(p, v);
-  }
-}
-
 }  // namespace wan

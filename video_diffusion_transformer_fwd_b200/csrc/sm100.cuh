@@ -378,6 +378,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
         "r"(r[15]) : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  uint32_t lo[16], hi[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) { lo[j] = r[j]; hi[j] = r[16 + j]; }
+  tmem_st16(taddr, lo);
+  tmem_st16(taddr + 16, hi);
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
