@@ -425,12 +425,12 @@ double split_cost(const LinArgs &g, int num_k, const Cut &c) {
 // of K takes its products (2 bn cycles) or its operands' way onto the SM (60
 // bytes a cycle, 28 from HBM: measured 560 cycles at bn = 256, 444 at 160), a
 // tile no less than its epilogue (9000 cycles at bn = 256, more with a residual,
-// 20000 where the rows of out or residual are out of the TMA unit's reach); the
+// 26000 and 35000 where the rows of out or residual are out of the TMA unit's reach); the
 // last one is in the open.
 double pair_cost(const LinArgs &g, int num_k, int bn) {
   const double tiles = ceil(g.M / 256.0) * ceil(g.N / (double)bn);
   const LinEpilogue e = lin_epilogue(g);
-  const double epi = 3000.0 + (e.vec_out && e.vec_res ? (g.res ? 8500.0 : 6000.0) : 17000.0) * bn / 256.0;
+  const double epi = 3000.0 + (e.vec_out && e.vec_res ? (g.res ? 8500.0 : 6000.0) : (g.res ? 32000.0 : 23000.0)) * bn / 256.0;
   // bytes of a step that no other tile has brought into L2
   const double cold = 64.0 * bn / ceil(g.M / 256.0) + W_BYTES * std::min(1.0, g.M / 256.0) / ceil(g.N / (double)bn);
   const double step = std::max(2.0 * bn, cold / 28.0 + std::max(0.0, W_BYTES + 64.0 * bn - cold) / 60.0);
