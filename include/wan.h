@@ -400,7 +400,10 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
  *             be the residual itself (same address, type and stride), and
  *             overlaps nothing else. What lies between its rows stays.
  * Products are accumulated in float32 on the tensor cores, everything after
- * them is float32, and the result is rounded once. A stride is ignored where
+ * them is float32, and the result is rounded once. (The tensor core rounds its
+ * sums toward zero: relative 1.1e-9 per element of K for WAN_BF16. For a
+ * WAN_F32 output K is summed in parts, most of them 768 and none above 4096,
+ * which are added in float32.) The same call gives the same bits every time. A stride is ignored where
  * its matrix has one row. No workspace. M or N = 0 is an empty call.
  * The first call on a device must come before any stream capture. The struct
  * is read during the call.
@@ -431,13 +434,14 @@ int wan_linear(const wan_linear_args *args, wan_stream_t stream);
  *             largest |y|: the codes that wan_quantize_fp8 gives for the
  *             float32 y, per row).
  *   row_scale float32 [rows], WAN_FP8 only: amax / 448 (a zero row: codes 0,
- *             scale 0; a row with a NaN or an infinity: scale and codes NaN).
+ *             scale 0; a row with a NaN or an infinity in h: scale and codes NaN).
  *   An output may be exactly an input matrix (same address, element size and
  *   stride: h_out = residual, y = x, ...), and overlaps nothing else. What
  *   lies between the rows of an output stays; what lies between the rows of
  *   an input may be read and has no effect.
- * h, the sum of squares, y and the scale are float32; the norm takes h before
- * it is rounded into h_out. rows = 0 is an empty call.
+ * h, the sum of squares, y and the scale are float32 (a sum of squares beyond
+ * its range gives y = 0); the norm takes h before it is rounded into h_out.
+ * rows = 0 is an empty call.
  * Errors: WAN_EINVAL (sizes, NULLs, strides below D, overlaps), WAN_EALIGN,
  * WAN_EUNSUPPORTED (D > 16384, dtypes). */
 typedef struct {

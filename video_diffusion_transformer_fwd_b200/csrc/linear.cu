@@ -22,7 +22,14 @@
 // barrier set-up and TMEM allocation then overlap the last CTAs of the kernel
 // before (one after another 1 x 5120 x 5120 takes 13.2 us, 16.4 without). Every
 // thread passes early_wait() before its first access to global memory, which
-// holds until the kernels before are done and their writes visible.
+// holds until the kernels before are done and their writes visible. (On the norm
+// and on CTA pairs, whose CTAs fill an SM, it cost time: 93600 x 128 10.7 ->
+// 13.2 us, 512 x 5120 x 4096 32.8 -> 33.2.)
+//
+// Measured: 1 x 5120 x 5120 bf16 12.9 us (4.1 TB/s of weights; 8.0 at the copy's
+// rate, and a launch is 2.4), 24 x 13824 x 5120 e4m3 16.6 us (4.3 TB/s), 333 x
+// 1003 x 1000 8.8 us, which is a launch, one trip to memory, the sums' exchange
+// and the epilogue.
 #include "common.cuh"
 #include "linear.cuh"
 #include "sm100.cuh"
@@ -407,7 +414,7 @@ Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
 // bytes a cycle from HBM (22 with one CTA) and 55 from L2 (an operand comes from
 // HBM for the first tile that reads it), and the card 3400 from HBM; SM and CTAs
 // need 400 cycles for a step of K at least; a token costs the epilogue 45, 70
-// with a residual. The cut or pair tile taken by these two costs was 2 to 6%
+// with a residual. The cut or pair tile taken by these two costs was 1 to 3%
 // slower in the mean than the best of all, over four sets of 26 random sizes.
 double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + c.mt - 1) / c.mt;
@@ -418,19 +425,19 @@ double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   const double step = ingest(W_BYTES, ntm) + ingest((double)std::min(c.mt, g.M) * ROW_BYTES, ntn);
   const double dram = ((double)g.M + g.N) * g.K * (g.fp8 ? 1 : 2) / 3400.0;
   const double waves = ceil(per_sm / resident(g, num_k, c)), finish = (g.res ? 70.0 : 45.0) * c.mt / (c.split > 1 ? 2.0 : 1.0);
-  return 8500.0 + waves * finish + 10.0 * c.mt * (per_sm - 1.0) + (c.split > 1 ? 2200.0 + 100.0 * c.split : 0.0) +
+  return 8500.0 + waves * finish + (800.0 + 10.0 * c.mt) * (per_sm - 1.0) + (c.split > 1 ? 4000.0 + 100.0 * c.split : 0.0) +
          4000.0 * (waves - 1.0) + std::max(std::max(per_sm * step, 400.0) * nkb, dram);
 }
 // The same of the pair kernel: tiles of 256 x bn in rounds of 74 pairs. A step
 // of K takes its products (2 bn cycles) or its operands' way onto the SM (60
 // bytes a cycle, 28 from HBM: measured 560 cycles at bn = 256, 444 at 160), a
 // tile no less than its epilogue (9000 cycles at bn = 256, more with a residual,
-// 26000 and 35000 where the rows of out or residual are out of the TMA unit's reach); the
-// last one is in the open.
+// 23000 and 31000 where the rows of out or residual are out of the TMA unit's
+// reach); the last one is in the open.
 double pair_cost(const LinArgs &g, int num_k, int bn) {
   const double tiles = ceil(g.M / 256.0) * ceil(g.N / (double)bn);
   const LinEpilogue e = lin_epilogue(g);
-  const double epi = 3000.0 + (e.vec_out && e.vec_res ? (g.res ? 8500.0 : 6000.0) : (g.res ? 32000.0 : 23000.0)) * bn / 256.0;
+  const double epi = 3000.0 + (e.vec_out && e.vec_res ? (g.res ? 8500.0 : 6000.0) : (g.res ? 28000.0 : 20000.0)) * bn / 256.0;
   // bytes of a step that no other tile has brought into L2
   const double cold = 64.0 * bn / ceil(g.M / 256.0) + W_BYTES * std::min(1.0, g.M / 256.0) / ceil(g.N / (double)bn);
   const double step = std::max(2.0 * bn, cold / 28.0 + std::max(0.0, W_BYTES + 64.0 * bn - cold) / 60.0);
