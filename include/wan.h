@@ -402,7 +402,7 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
  * Products are accumulated in float32 on the tensor cores, everything after
  * them is float32, and the result is rounded once. (The tensor core rounds its
  * sums toward zero: relative 1.1e-9 per element of K for WAN_BF16. For a
- * WAN_F32 output K is summed in parts, most of them 768 and none above 4096,
+ * WAN_F32 output K is summed in parts, most of them 768 and none above 2048,
  * which are added in float32.) The same call gives the same bits every time. A stride is ignored where
  * its matrix has one row. No workspace. M or N = 0 is an empty call.
  * The first call on a device must come before any stream capture. The struct

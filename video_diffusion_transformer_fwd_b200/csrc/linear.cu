@@ -460,6 +460,9 @@ Choice choose(const LinArgs &g) {
     if (tiles > 65535) continue;
     for (int split = 1; split <= std::min(MAX_SPLIT, num_k); ++split) {
       const Cut c = {mt, split};
+      // parts of K no longer than the longest on CTA pairs
+      const int nkb = (num_k + split - 1) / split;
+      if (lin_parts(g, nkb) > 1 && nkb > 32 * accumulators_of(g, num_k, c)) continue;
       const double cost = split_cost(g, num_k, c);
       if (!cut.mt || cost < best) { best = cost; cut = c; }
     }
