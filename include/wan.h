@@ -398,7 +398,9 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
  *             after the activation; NULL: none.
  *   out       [M, N] in out_dtype (WAN_BF16 or WAN_F32), rows ldo apart. May
  *             be the residual itself (same address, type and stride), and
- *             overlaps nothing else. What lies between its rows stays.
+ *             overlaps nothing else; slices of one packed buffer (the same
+ *             stride, columns of their own) do not overlap. What lies between
+ *             its rows stays.
  * Products are accumulated in float32 on the tensor cores, everything after
  * them is float32, and the result is rounded once. (The tensor core rounds its
  * sums toward zero: relative 1.1e-9 per element of K for WAN_BF16. For a
@@ -408,7 +410,7 @@ int wan_linear_fp8(int M, int N, int K, const uint8_t *a, const float *a_scale, 
  * The first call on a device must come before any stream capture. The struct
  * is read during the call.
  * Errors: WAN_EINVAL (sizes, NULLs, strides below the width, overlaps),
- * WAN_EALIGN (pointers, lda, ldw), WAN_EUNSUPPORTED (dtypes, activation). */
+ * WAN_EALIGN (pointers: 16 bytes, a_scale and a single w_scale 4; lda, ldw), WAN_EUNSUPPORTED (dtypes, activation). */
 typedef struct {
   const void *a, *w;
   const float *a_scale, *w_scale;
@@ -436,13 +438,15 @@ int wan_linear(const wan_linear_args *args, wan_stream_t stream);
  *   row_scale float32 [rows], WAN_FP8 only: amax / 448 (a zero row: codes 0,
  *             scale 0; a row with a NaN or an infinity in h: scale and codes NaN).
  *   An output may be exactly an input matrix (same address, element size and
- *   stride: h_out = residual, y = x, ...), and overlaps nothing else. What
+ *   stride: h_out = residual, y = x, ...), and overlaps nothing else; slices of
+ *   one packed buffer (the same stride, columns of their own) do not overlap. What
  *   lies between the rows of an output stays; what lies between the rows of
  *   an input may be read and has no effect.
  * h, the sum of squares, y and the scale are float32 (a sum of squares beyond
  * its range gives y = 0); the norm takes h before it is rounded into h_out.
  * rows = 0 is an empty call.
- * Errors: WAN_EINVAL (sizes, NULLs, strides below D, overlaps), WAN_EALIGN,
+ * Errors: WAN_EINVAL (sizes, NULLs, strides below D, overlaps), WAN_EALIGN
+ * (pointers: 16 bytes, row_scale 4),
  * WAN_EUNSUPPORTED (D > 16384, dtypes). */
 typedef struct {
   const void *x, *residual;

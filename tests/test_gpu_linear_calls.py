@@ -118,3 +118,30 @@ def test_after_a_wait_that_gave_up(M, N, K, f8):
     assert wan.wan_device_status(s) == wan.WAN_OK
     c.check(c.run())
     assert wan.device_status() == wan.WAN_OK
+
+
+@pytest.mark.parametrize("rows", [1, 6, 700])
+@pytest.mark.parametrize("D", [128, 136])
+def test_slices_of_one_buffer(rows, D):
+    """Inputs and outputs side by side in the rows of a packed buffer, and scales
+    that begin at any row."""
+    g = torch.Generator(device="cuda").manual_seed(rows + D)
+    buf = torch.randn(rows, 3 * D + 40, device="cuda", generator=g).bfloat16()
+    w = torch.randn(D, D, device="cuda", generator=g).bfloat16()
+    before = buf.clone()
+    a, y, out, rest = buf[:, :D], buf[:, D:2 * D], buf[:, 2 * D:3 * D], buf[:, 3 * D:]
+    want, _, _ = wan.rmsnorm(a.clone())
+    wan.rmsnorm(a, out=y)
+    assert torch.equal(y, want)
+    wan.linear(y, w, residual=a, out=out)
+    assert torch.equal(out, wan.linear(want, w, residual=before[:, :D].contiguous()))
+    assert torch.equal(a, before[:, :D]) and torch.equal(rest, before[:, 3 * D:])
+    if rows > 5 and D % 16 == 0:
+        q, s = wan.quantize_fp8(want)
+        wq, ws = wan.quantize_fp8(w, per_row=False)
+        full = wan.linear(q, wq, a_scale=s, w_scale=ws)
+        part = wan.linear(q[3:], wq, a_scale=s[3:], w_scale=ws)
+        assert float((part.float() - full[3:].float()).norm()) <= 2.0 ** -8 * float(full.float().norm())
+        scales = torch.zeros(rows, device="cuda")
+        wan.rmsnorm(want[:rows - 1].contiguous(), out_dtype="fp8", row_scale=scales[1:])
+        assert scales[0] == 0 and (scales[1:] > 0).all()

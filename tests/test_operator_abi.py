@@ -34,12 +34,15 @@ def norm(**kw):
     (dict(ldx=63), EINVAL), (dict(ldr=63), EINVAL), (dict(ldh=63), EINVAL), (dict(ldy=63), EINVAL),
     (dict(ldx=-64), EINVAL), (dict(ldx=1 << 62), EINVAL),
     (dict(x=MB + 2), EALIGN), (dict(residual=2 * MB + 4), EALIGN), (dict(gain=3 * MB + 4), EALIGN),
-    (dict(h_out=4 * MB + 8), EALIGN), (dict(y=5 * MB + 1), EALIGN), (dict(row_scale=6 * MB + 4), EALIGN),
+    (dict(h_out=4 * MB + 8), EALIGN), (dict(y=5 * MB + 1), EALIGN), (dict(row_scale=6 * MB + 2), EALIGN),
     (dict(y=MB), EINVAL),                                                # codes over bf16 x
     (dict(y=2 * MB + 16), EINVAL), (dict(h_out=2 * MB + 16), EINVAL),    # partial overlap with the residual
     (dict(h_out=2 * MB, ldh=72), EINVAL),                                # another stride than the residual it covers
     (dict(h_out=5 * MB), EINVAL),                                        # two outputs in one place
     (dict(row_scale=5 * MB + 16), EINVAL), (dict(y=3 * MB), EINVAL),     # over the gain
+    # slices of one buffer that reach into each other's columns, directly or around the end of a row
+    (dict(x=MB, ldx=128, y=MB + 112, ldy=256), EINVAL), (dict(x=MB, ldx=128, y=MB + 208, ldy=256), EINVAL),
+    (dict(x=MB, ldx=128, y=MB + 128, ldy=128), EINVAL),                  # beside it, but another stride
     (dict(rows=0), OK), (dict(rows=0, x=None, y=None), OK),
 ])
 def test_rmsnorm_refusals(kw, code):
@@ -65,7 +68,8 @@ def lin(**kw):
     (dict(dtype=wan.WAN_BF16, lda=68), EALIGN), (dict(dtype=wan.WAN_BF16, ldw=68), EALIGN),
     (dict(lda=48), EINVAL), (dict(ldw=48), EINVAL), (dict(ldr=47), EINVAL), (dict(ldo=47), EINVAL),
     (dict(a=MB + 8), EALIGN), (dict(w=3 * MB + 8), EALIGN), (dict(bias=5 * MB + 2), EALIGN), (dict(out=7 * MB + 4), EALIGN),
-    (dict(a_scale=2 * MB + 4), EALIGN), (dict(w_scale=4 * MB + 4), EALIGN), (dict(residual=6 * MB + 4), EALIGN),
+    (dict(a_scale=2 * MB + 2), EALIGN), (dict(w_scale=4 * MB + 4), EALIGN),
+    (dict(w_scale=4 * MB + 2, w_scale_rows=0), EALIGN), (dict(residual=6 * MB + 4), EALIGN),
     (dict(out=1 * MB), EINVAL), (dict(out=3 * MB), EINVAL), (dict(out=5 * MB), EINVAL), (dict(out=4 * MB), EINVAL),
     (dict(out=6 * MB + 16), EINVAL), (dict(out=6 * MB, ldo=64), EINVAL),
     (dict(out=6 * MB, out_dtype=wan.WAN_BF16), EINVAL),                  # another type than the residual it covers

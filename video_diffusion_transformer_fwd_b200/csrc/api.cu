@@ -541,8 +541,19 @@ struct Extent {
   size_t es;
   long long ld, width;
   bool required, output;
-  int rows = 0;
+  int rows = 0, align = 16;
 };
+
+// Rows of a and b that take turns in memory: the same stride, each in its own
+// columns of it (slices of one packed buffer).
+static bool side_by_side(const Extent &a, const Extent &b) {
+  if (a.ld <= 0 || a.ld > LLONG_MAX / 8 || b.ld <= 0 || b.ld > LLONG_MAX / 8) return false;   // a single row's, unchecked
+  const long long stride = a.ld * (long long)a.es, wa = a.width * (long long)a.es, wb = b.width * (long long)b.es;
+  if (stride != b.ld * (long long)b.es) return false;
+  long long d = ((long long)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p))) % stride;
+  if (d < 0) d += stride;
+  return d >= wa && d + wb <= stride;
+}
 
 // NULLs, alignment, row strides, and outputs that overlap another argument. An
 // output may be exactly an input (same address, element size and stride: every
@@ -556,7 +567,8 @@ static int check_extents(const char *op, const Extent *e, size_t n, int rows, co
       if (e[i].required) return set_error(WAN_EINVAL, "%s: %s is NULL", op, e[i].name);
       continue;
     }
-    if (!aligned16(e[i].p)) return set_error(WAN_EALIGN, "%s: %s not 16-byte aligned", op, e[i].name);
+    if (reinterpret_cast<uintptr_t>(e[i].p) % e[i].align)
+      return set_error(WAN_EALIGN, "%s: %s not %d-byte aligned", op, e[i].name, e[i].align);
     const long long r = e[i].rows ? e[i].rows : rows;
     if (r > 1 && e[i].ld < e[i].width)
       return set_error(WAN_EINVAL, "%s: row stride %lld of %s is below its width %lld", op, e[i].ld, e[i].name, e[i].width);
@@ -568,7 +580,7 @@ static int check_extents(const char *op, const Extent *e, size_t n, int rows, co
     for (size_t i = 0; i < n; ++i) {
       if (i == o || !e[i].p || (e[i].output && i < o)) continue;
       const char *a = static_cast<const char *>(e[o].p), *b = static_cast<const char *>(e[i].p);
-      if (!(a < hi[i] && b < hi[o])) continue;
+      if (!(a < hi[i] && b < hi[o]) || side_by_side(e[o], e[i])) continue;
       const bool same = a == b && e[o].es == e[i].es && (rows == 1 || e[o].ld == e[i].ld) && e[o].width == e[i].width &&
                         !e[i].output && e[i].rows == 0;
       if (!same || (in_place && strcmp(in_place, e[i].name)))
@@ -747,12 +759,13 @@ int wan_rmsnorm(const wan_rmsnorm_args *args, wan_stream_t stream) {
   const Extent ex[] = {{"x", x, xs, ldx, D, true, false}, {"residual", residual, rs, ldr, D, false, false},
                        {"gain", gain, 4, D, D, false, false, 1}, {"y", y, ys, ldy, D, true, true},
                        {"h_out", h_out, rs, ldh, D, false, true},
-                       {"row_scale", y_dtype == WAN_FP8 ? row_scale : nullptr, 4, 1, 1, y_dtype == WAN_FP8, true}};
+                       {"row_scale", y_dtype == WAN_FP8 ? row_scale : nullptr, 4, 1, 1, y_dtype == WAN_FP8, true, 0, 4}};
   int rc = check_extents("rmsnorm", ex, sizeof(ex) / sizeof(ex[0]), rows);
   if (rc) return rc;
   cudaStream_t s = (cudaStream_t)stream;
-  return WAN_PROF(WAN_K_LAYERNORM, s, launch_rmsnorm(rows, D, x, x_dtype, ldx, residual, res_dtype, ldr, gain, eps, h_out,
-                                                     ldh, y, y_dtype, ldy, row_scale, s));
+  const wan_rmsnorm_args &q = *args;
+  return WAN_PROF(WAN_K_LAYERNORM, s, launch_rmsnorm(q.rows, q.D, q.x, q.x_dtype, q.ldx, q.residual, q.res_dtype, q.ldr,
+                                                     q.gain, q.eps, q.h_out, q.ldh, q.y, q.y_dtype, q.ldy, q.row_scale, s));
 }
 
 int wan_linear(const wan_linear_args *args, wan_stream_t stream) {
@@ -778,8 +791,8 @@ int wan_linear(const wan_linear_args *args, wan_stream_t stream) {
   if (lda % pad || ldw % pad)
     return set_error(WAN_EALIGN, "linear: the rows of a and w must start on 16-byte boundaries (lda %lld, ldw %lld)", lda, ldw);
   const Extent ex[] = {{"a", a, es, lda, K, true, false}, {"w", w, es, ldw, K, true, false, N},
-                       {"a_scale", f8 ? a_scale : nullptr, 4, 1, 1, f8, false},
-                       {"w_scale", f8 ? w_scale : nullptr, 4, 1, 1, f8, false, f8 && w_scale_rows ? N : 1},
+                       {"a_scale", f8 ? a_scale : nullptr, 4, 1, 1, f8, false, 0, 4},
+                       {"w_scale", f8 ? w_scale : nullptr, 4, 1, 1, f8, false, f8 && w_scale_rows ? N : 1, f8 && w_scale_rows ? 16 : 4},
                        {"bias", bias, 2, N, N, false, false, 1}, {"residual", residual, rs, ldr, N, false, false},
                        {"out", out, os, ldo, N, true, true}};
   int rc = check_extents("linear", ex, sizeof(ex) / sizeof(ex[0]), M, "residual");
