@@ -400,6 +400,12 @@ class _Types:
         return cls.codes
 
 
+def _float_code(codes, t):
+    """dtype_code through the dict."""
+    code = codes.get(t.dtype, WAN_FP8)
+    return dtype_code(t) if code == WAN_FP8 else code
+
+
 # Small calls are bound by the host: the helpers of wan_rmsnorm and wan_linear
 # look at each tensor once and make one library call.
 def _matrix(t, name, shape, rows, dev):
@@ -465,7 +471,7 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
         raise ValueError("x needs a last axis to normalise")
     D = shape[-1]
     rows = x.numel() // D
-    xc = dtype_code(x)
+    xc = _float_code(codes, x)
     if out is None:
         code = xc if out_dtype is None else DTYPE_CODES[out_dtype]
         out = _empty_on(stream, shape, {WAN_FP8: torch.uint8, WAN_BF16: torch.bfloat16, WAN_F32: torch.float32}[code], x.device)
@@ -485,7 +491,7 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
         raise ValueError("row_scale goes with e4m3 codes")
     rc, rp, ldr, hp, ldh = WAN_F32, 0, 0, 0, 0
     if residual is not None:
-        rc = dtype_code(residual)
+        rc = _float_code(codes, residual)
         rp, ldr = _matrix(residual, "residual", shape, rows, dev)
         if h_out is None:
             h_out = _empty_on(stream, shape, residual.dtype, x.device)
@@ -549,10 +555,11 @@ def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_sc
     bp = 0 if bias is None else _vector(bias, "bias", N, torch.bfloat16, dev)
     rc, rp, ldr = WAN_F32, 0, 0
     if residual is not None:
-        rc = dtype_code(residual)
+        rc = _float_code(codes, residual)
         rp, ldr = _matrix(residual, "residual", shape, M, dev)
     check(load().wan_linear(_LINEAR_ARGS.pack(ap, wp, asp, wsp, bp, rp, op, lda, ldw, ldr, ldo, M, N, K, code, per_row,
-                                              ACTIVATIONS[activation], rc, dtype_code(out)), _raw_stream(stream, dev)))
+                                              ACTIVATIONS[activation], rc, _float_code(codes, out)),
+                            _raw_stream(stream, dev)))
     return out
 
 
