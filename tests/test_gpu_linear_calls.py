@@ -145,3 +145,23 @@ def test_slices_of_one_buffer(rows, D):
         scales = torch.zeros(rows, device="cuda")
         wan.rmsnorm(want[:rows - 1].contiguous(), out_dtype="fp8", row_scale=scales[1:])
         assert scales[0] == 0 and (scales[1:] > 0).all()
+
+
+@pytest.mark.parametrize("M,N", [(5984, 155), (5000, 153), (5000, 158), (4000, 1001), (2600, 2559), (64, 155)])
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_rows_that_end_inside_16_bytes(M, N, res, out):
+    """Rows that begin on 16-byte boundaries and end inside one: what lies behind
+    them stays, with a residual of its own and with one in place."""
+    c = Case(M, N, 520, act="relu", res=res, out=out)
+    ld = (N + 7) // 8 * 8
+    full = torch.full((M, ld), 7.0, device="cuda", dtype=c.out)
+    o = full[:, :N]
+    kw = {}
+    if res == out:
+        o.copy_(c.r)
+        kw = dict(residual=o)
+    c.run(out=o, **kw)
+    assert (full[:, N:] == 7).all()
+    c.check(o, list(range(0, M, max(1, M // 100))))
+    assert wan.device_status() == wan.WAN_OK

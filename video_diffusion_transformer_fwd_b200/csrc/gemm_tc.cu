@@ -137,8 +137,8 @@ __device__ __forceinline__ float bf16_bits_to_float(uint32_t lo16) {
 // which is now at 150 (1.43 PFLOP/s), its products alone at 141. The residual of a chunk is asked for when the
 // chunk before it has been added, the first one of a tile during the last of
 // the tile before. Outputs (or residuals) whose rows do not start on 16-byte
-// boundaries are turned around in shared memory instead and stored a column
-// per lane.
+// boundaries, and the last chunk of rows that end inside 16 bytes, are turned
+// around in shared memory instead and stored a column per lane.
 template <bool F8>
 struct LinearEpilogue {
   using G = Geo<false, true>;
@@ -231,6 +231,7 @@ struct LinearEpilogue {
   // rows that the TMA unit cannot address: column `lane` of the chunk, row by row
   __device__ __forceinline__ void store_by_columns(const float (&v)[32], int m0, int n) {
     uint8_t *tile = tiles + STG_BYTES;
+    if (lane == 0) bulk_wait_group_read<0>();    // an earlier chunk's store has read the tile
     __syncwarp();
 #pragma unroll
     for (int g = 0; g < 8; ++g)
@@ -276,6 +277,9 @@ struct LinearEpilogue {
     constexpr int nbuf = G::NACC;
     const int buf_cols = p.parts > 1 ? p.bn : G::BN, chunks = p.bn / 32;
     const bool tma_out = e.vec_out;
+    // the TMA unit writes whole groups of 16 bytes: a row that ends inside one
+    // would take what lies behind it along
+    const bool ragged = p.N % (e.out_f32 ? 4 : 8) != 0;
     tma_res = e.res && e.vec_res;
     int stores = 0;
     rt = pair; rc = half - 2;
@@ -373,7 +377,7 @@ struct LinearEpilogue {
         }
         lin_act_row(v, e.act);
         if (tma_res && !add_residual(v)) return;
-        if (!tma_out || (e.res && !tma_res)) { store_by_columns(v, m0, n); continue; }
+        if (!tma_out || (e.res && !tma_res) || (ragged && n + 32 > p.N)) { store_by_columns(v, m0, n); continue; }
         // with a residual the second tile alone holds the output, else both in turn
         uint8_t *tile = tiles + (e.res || (stores & 1) ? STG_BYTES : 0);
         if (lane == 0) {                         // this tile's previous store has read it
