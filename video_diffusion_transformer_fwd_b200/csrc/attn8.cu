@@ -384,7 +384,7 @@ attn8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     if (!(crow > 0.f)) crow = 1e-30f;
     bool ok = true;
     for (int j = 0; j < nkt; ++j) {
-      if (!mbar_wait(smem_u32(&s_full[i]), j & 1, abort_flag, p.watchdog, 0x321)) { ok = false; break; }
+      if (!mbar_wait_warp(smem_u32(&s_full[i]), j & 1, abort_flag, p.watchdog, 0x321)) { ok = false; break; }
       tc_fence_after();
       uint32_t s[128];
 #pragma unroll
@@ -439,7 +439,7 @@ attn8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       const float2 acc = fadd2(acc0, acc1);
       l = l * alpha + (acc.x + acc.y);
       if (j > 0 && __any_sync(0xffffffffu, need)) {
-        if (!mbar_wait(smem_u32(&pv_done[i]), (j - 1) & 1, abort_flag, p.watchdog, 0x322)) ok = false;
+        mbar_wait_lanes(ok, smem_u32(&pv_done[i]), (j - 1) & 1, abort_flag, p.watchdog, 0x322);
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
@@ -456,11 +456,10 @@ attn8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&p_ready[i]));
-      if (!ok) break;
     }
     // epilogue: O / l times the channel scales of v -> bf16
-    if (ok && nkt > 0) {
-      ok = mbar_wait(smem_u32(&pv_done[i]), (nkt - 1) & 1, abort_flag, p.watchdog, 0x323);
+    if (nkt > 0) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&pv_done[i]), (nkt - 1) & 1, abort_flag, p.watchdog, 0x323));
       tc_fence_after();
     }
     const float inv = (l > 0.f) ? 1.0f / l : 0.f;

@@ -284,7 +284,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
     bool ok = true;
     for (int j = 0; j < nkt; ++j) {
-      if (!mbar_wait(smem_u32(&s_full[i]), j & 1, abort_flag, p.watchdog, 0x221)) { ok = false; break; }
+      if (!mbar_wait_warp(smem_u32(&s_full[i]), j & 1, abort_flag, p.watchdog, 0x221)) { ok = false; break; }
       tc_fence_after();
       uint32_t s[128];
 #pragma unroll
@@ -331,7 +331,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       l = l * alpha + (acc.x + acc.y);
       // P_i and O_i are still in use by PV_i(j-1) until it completes
       if (j > 0) {
-        if (!mbar_wait(smem_u32(&pv_done[i]), (j - 1) & 1, abort_flag, p.watchdog, 0x222)) ok = false;
+        mbar_wait_lanes(ok, smem_u32(&pv_done[i]), (j - 1) & 1, abort_flag, p.watchdog, 0x222);
         tc_fence_after();
       }
       // O rescale (TMEM accesses are warp-collective: a warp rescales when
@@ -358,11 +358,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&p_full[i]));
-      if (!ok) break;
     }
     // epilogue: O / l -> bf16
-    if (ok && nkt > 0) {
-      ok = mbar_wait(smem_u32(&pv_done[i]), (nkt - 1) & 1, abort_flag, p.watchdog, 0x223);
+    if (nkt > 0) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&pv_done[i]), (nkt - 1) & 1, abort_flag, p.watchdog, 0x223));
       tc_fence_after();
     }
     // O / l as bf16 into the P_i tile (free once PV_i of the last key tile is

@@ -182,8 +182,7 @@ struct LinearEpilogue {
 
   // v += the residual of the chunk
   __device__ __forceinline__ bool add_residual(float (&v)[32]) {
-    const bool ok = mbar_wait(rbar, taken & 1, abort_flag, p.watchdog, 0x123);
-    if (!__all_sync(0xffffffffu, ok)) return false;
+    if (!mbar_wait_warp(rbar, taken & 1, abort_flag, p.watchdog, 0x123)) return false;
     ++taken;
     if (e.res_f32) {
 #pragma unroll
@@ -327,8 +326,7 @@ struct LinearEpilogue {
       const bool summed = p.parts > 1;
       for (int part = 0; summed && part < p.parts; ++part, ++i) {
         const int buf = i % nbuf;
-        const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122);
-        if (!__all_sync(0xffffffffu, ready)) return;
+        if (!mbar_wait_warp(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122)) return;
         tc_fence_after();
 #pragma unroll 1
         for (int c = half; c < chunks; c += 2) {
@@ -341,8 +339,7 @@ struct LinearEpilogue {
       }
       const int buf = i % nbuf;
       if (!summed) {
-        const bool ready = mbar_wait(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122);
-        if (!__all_sync(0xffffffffu, ready)) return;
+        if (!mbar_wait_warp(smem_u32(&tfull[buf]), (i / nbuf) & 1, abort_flag, p.watchdog, 0x122)) return;
         ++i;
         tc_fence_after();
       }
@@ -411,7 +408,7 @@ struct LinearEpilogue {
   // a residual tile still in flight (after a wait gave up) lands before the CTA ends
   __device__ __forceinline__ void drain() {
     int never = 0;
-    if (tma_res && taken < asked) mbar_wait(rbar, taken & 1, &never, p.watchdog, 0x124);
+    if (tma_res && taken < asked) mbar_wait_warp(rbar, taken & 1, &never, p.watchdog, 0x124);
   }
 };
 
@@ -491,7 +488,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     uint32_t phase = 0;
     long long loads = 0;
     bool ok = true;
-    for (int t = pair; t < p.num_tiles && ok; t += npairs) {
+    for (int t = pair; t < p.num_tiles; t += npairs) {
       int mb, nb;
       tile_coords(t, p, mb, nb);
       const int n0 = nb * BN;
@@ -500,8 +497,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int a_row = mb * 2 * BM + (int)rank * BM;
       const int b_row = n0 - seg * p.segN + (int)rank * (LIN ? BN / 2 : 128);   // this CTA's rows of each N = 256 half (of bn)
       for (int kb = 0; kb < p.num_k; ++kb) {
-        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101)) { ok = false; break; }
-        if (elect_one()) {
+        mbar_wait_lanes(ok, smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101);
+        if (elect_one() && ok) {
           const uint32_t fb_local = smem_u32(&full[stage]);
           if (leader) mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
           const uint32_t fb = mapa_shared(fb_local, 0);
@@ -511,14 +508,14 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (WIDE)      // the second N = 256 half of the tile: B rows 256 further
             tma_load_2d_pair(smem_u32(sB + stage * B_BYTES + B_BYTES / 2), bm, kx, b_row + 256, fb);
         }
-        ++loads;
+        if (ok) ++loads;
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     }
     // drain (leader): every issued copy of the pair has landed before exit.
     // The peer's copies complete on the leader's barrier, so the leader's
     // drain also covers them; the final cluster barrier orders the rest.
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       int never = 0;
       for (int s = 0; s < STAGES; ++s) {
         const long long fills = loads > s ? (loads - 1 - s) / STAGES + 1 : 0;
@@ -533,23 +530,23 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       uint32_t phase = 0;
       int i = 0;
       bool ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
-        for (int part = 0; part < parts && ok; ++part, ++i) {
+      for (int t = pair; t < p.num_tiles; t += npairs) {
+        for (int part = 0; part < parts; ++part, ++i) {
           const int buf = i % nbuf;
           const uint32_t acc_phase = (i / nbuf) & 1;
-          if (!mbar_wait(smem_u32(&tempty[buf]), acc_phase ^ 1, abort_flag, p.watchdog, 0x111)) { ok = false; break; }
+          mbar_wait_lanes(ok, smem_u32(&tempty[buf]), acc_phase ^ 1, abort_flag, p.watchdog, 0x111);
           tc_fence_after();
           const uint32_t d = tmem_base + buf * buf_cols;
           const int kb0 = LIN ? part * p.part_steps : 0, kb1 = LIN ? min(p.num_k, kb0 + p.part_steps) : p.num_k;
           for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112)) { ok = false; break; }
+            mbar_wait_lanes(ok, smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112);
             tc_fence_after();
             const int first = kb - kb0;
             const uint64_t a0 = desc_kmajor_sw128(smem_u32(sA + stage * A_BYTES));
             const uint64_t b0 = desc_kmajor_sw128(smem_u32(sB + stage * B_BYTES));
             // 4 MMAs of 32 bytes of K per stage (16 bf16 or 32 e4m3 each):
             // the descriptor start address advances 32 bytes (2 in 16-byte units)
-            if (elect_one()) {
+            if (elect_one() && ok) {
 #pragma unroll
               for (int h = 0; h < G::BN / 256; ++h) {
                 // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
@@ -566,7 +563,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
           }
-          if (ok && elect_one()) tc_commit_both(smem_u32(&tfull[buf]));
+          if (elect_one() && ok) tc_commit_both(smem_u32(&tfull[buf]));
         }
       }
     }
@@ -650,7 +647,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           prefetch_l1(rw + 344); prefetch_l1(rw + 464); prefetch_l1(rw + 504);
         }
       }
-      if (!mbar_wait(smem_u32(&tfull[buf]), acc_phase, abort_flag, p.watchdog, 0x121)) break;
+      if (!mbar_wait_warp(smem_u32(&tfull[buf]), acc_phase, abort_flag, p.watchdog, 0x121)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {

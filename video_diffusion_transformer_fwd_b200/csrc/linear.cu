@@ -209,13 +209,15 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     // ------------------------------------------------ TMA producer
     int stage = ahead == p.stages ? 0 : ahead, issued = ahead;
     uint32_t phase = 0;
-    for (; issued < nkb; ++issued) {
-      if (!mbar_wait(smem_u32(&empty[stage]), phase, &abort_flag, p.watchdog, 0x201)) break;
-      if (elect_one()) load(issued, stage);
+    bool ok = true;
+    for (int i = ahead; i < nkb; ++i) {
+      mbar_wait_lanes(ok, smem_u32(&empty[stage]), phase, &abort_flag, p.watchdog, 0x201);
+      if (elect_one() && ok) load(i, stage);
+      if (ok) ++issued;
       if (++stage == p.stages) { stage = 0; phase ^= 1; }
     }
     // every copy issued has landed before the CTA ends
-    if (lane == 0) {
+    if (elect_one()) {
       int never = 0;
       for (int s = 0; s < p.stages; ++s) {
         const int fills = issued > s ? (issued - 1 - s) / p.stages + 1 : 0;
@@ -236,7 +238,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     const uint32_t ring = smem_u32(smem), f0 = smem_u32(full);
     bool next = mbar_try_wait(f0, 0);
     for (int i = 0, in_chunk = 0, acc = 0; i < nkb; ++i) {
-      if (!next && !mbar_wait(f0 + 8 * stage, phase, &abort_flag, p.watchdog, 0x211)) { ok = false; break; }
+      if (!next) mbar_wait_lanes(ok, f0 + 8 * stage, phase, &abort_flag, p.watchdog, 0x211);
       tc_fence_after();
       const uint32_t base = ring + stage * stage_bytes;
       const uint64_t aw = desc_kmajor_sw128(base);
@@ -244,7 +246,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       const uint32_t d = tmem + acc * p.mt, eb = smem_u32(empty) + 8 * stage;
       if (++stage == p.stages) { stage = 0; phase ^= 1; }
       next = i + 1 < nkb && mbar_try_wait(f0 + 8 * stage, phase);     // asked ahead of the products' issue
-      if (elect_one()) {
+      if (elect_one() && ok) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {       // 32 bytes of K each: + 2 in 16-byte units
           const uint32_t add = (in_chunk | kk) != 0;
@@ -255,7 +257,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       }
       if (++in_chunk == p.chunk) { in_chunk = 0; ++acc; }
     }
-    if (ok && elect_one()) tc_commit(smem_u32(&done));
+    if (elect_one() && ok) tc_commit(smem_u32(&done));
     __syncwarp();
     if (split > 1) {
       if (!early) cluster_arrive();
@@ -274,8 +276,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     const float ws = F8 && n < p.N ? e.w_scale[e.w_scale_rows ? n : 0] : 1.f;
     Finish<F8> f{e, m0, rows, n, p.N, rank, split, bias, ws};
     f.fetch(0);
-    bool ok = mbar_wait(smem_u32(&done), 0, &abort_flag, p.watchdog, 0x221);
-    ok = __all_sync(0xffffffffu, ok);
+    bool ok = mbar_wait_warp(smem_u32(&done), 0, &abort_flag, p.watchdog, 0x221);
     tc_fence_after();
     // sums from rank r of the i-th group of this CTA: recv + (r * most + i) * GROUP_BYTES
     const int most = (groups + split - 1) / split;
@@ -301,8 +302,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       cluster_arrive();                      // nothing more leaves this warp
       if (mine > 0) {
         int never = 0;
-        const bool all = mbar_wait_cluster(smem_u32(&arrived), 0, &never, p.watchdog, 0x222);
-        ok = __all_sync(0xffffffffu, ok && all);
+        if (!mbar_wait_cluster(smem_u32(&arrived), 0, &never, p.watchdog, 0x222)) ok = false;
       }
     }
     if (ok) {

@@ -81,10 +81,31 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// mbar_wait on a barrier that other CTAs of the cluster complete.
+// mbar_wait is for one thread: of two lanes at the end of a wait one may give up
+// and the other see the phase complete. What follows in a warp (elect.sync,
+// tcgen05.ld, __syncwarp) waits for every lane, without a limit, so the lanes
+// have to go on together or stop together. A warp therefore waits in one of two
+// ways. mbar_wait_warp: one answer for all lanes, by a vote.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, int *watchdog,
+                                               int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, watchdog, code));
+}
+
+// mbar_wait_lanes: a lane that gives up clears its own `ok` and goes on beside
+// the others, without waiting any more. Loops that run in all lanes for the sake
+// of one that issues (elect_one) wait so: they end by their counts alone, and a
+// step is issued where the elected lane, the same one every time, is still ok.
+// (A vote at every step costs wan_linear's split kernel more: 333 x 1003 x 1000
+// 9.1 us, 8.7 this way.)
+__device__ __forceinline__ void mbar_wait_lanes(bool &ok, uint32_t bar, uint32_t parity, volatile int *abort,
+                                                int *watchdog, int code) {
+  if (ok && !mbar_wait(bar, parity, abort, watchdog, code)) ok = false;
+}
+
+// mbar_wait_warp on a barrier that other CTAs of the cluster complete.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort, int *watchdog,
                                                   int code) {
-  const bool ok = mbar_wait(bar, parity, abort, watchdog, code);
+  const bool ok = mbar_wait_warp(bar, parity, abort, watchdog, code);
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
   return ok;
 }
