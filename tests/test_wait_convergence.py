@@ -1,4 +1,4 @@
-"""Bounded waits of the kernels, read from their sources (no GPU needed).
+"""Bounded waits of the kernels and lanes that leave their warp, read from their sources (no GPU needed).
 
 mbar_wait answers each thread for itself, so the lanes of a warp may leave one
 at the end of its limit with different answers. The instructions that follow in
@@ -57,3 +57,12 @@ def test_the_reader_tells_the_two_apart():
 def test_warps_wait_with_one_answer(name):
     with open(os.path.join(CSRC, name)) as f:
         assert waits_of_several_threads(f.read()) == []
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_no_lane_leaves_its_warp(name):
+    """No return, break or continue that a lane takes for itself: what comes
+    after it in the warp is executed by all lanes or by none."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = plain(f.read())
+    assert re.findall(r"if \([^;{}]*\b(?:lane|threadIdx\.x)\b[^;{}]*\) (?:return|break|continue)\b", text) == []

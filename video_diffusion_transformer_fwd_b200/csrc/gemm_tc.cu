@@ -236,8 +236,7 @@ struct LinearEpilogue {
     for (int g = 0; g < 8; ++g)
       *reinterpret_cast<float4 *>(slot(tile, lane, g)) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
     __syncwarp();
-    if (n + lane >= p.N) return;
-    const int rows = min(32, p.M - m0);
+    const int rows = n + lane < p.N ? min(32, p.M - m0) : 0;      // lanes past the end: none
     // 16 rows at a time, all loads of the residual before the first store (rows
     // past the end read the last one): one by one behind the choice of the type
     // each waited for the one before
@@ -268,6 +267,7 @@ struct LinearEpilogue {
       for (int r = 0; r < 16; ++r)
         if (r0 + r < rows) lin_put(e, m0 + r0 + r, n + lane, o[r]);
     }
+    __syncwarp();                                // the next tcgen05.ld is the whole warp's
   }
 
   // returns when all tiles are done, or a wait gave up
