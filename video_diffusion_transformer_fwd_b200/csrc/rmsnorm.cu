@@ -36,6 +36,8 @@
 
 #include <float.h>
 
+#include <atomic>
+
 namespace wan {
 
 namespace {
@@ -355,6 +357,7 @@ __device__ __forceinline__ void pieces_out(T *p, const uint8_t *buf, int n) {
 
 constexpr int RAGGED_NV = 16;                              // most elements of a thread
 constexpr int RAGGED_CTA = RMS_MAX_D / RAGGED_NV;
+constexpr int RAGGED_SHORT_D = 4096;                       // widest row that takes 8 elements a thread
 
 // One CTA per row, NV elements a thread (every blockDim-th). Two buffers: x in,
 // then y out; r in, then h out.
@@ -435,13 +438,30 @@ int rms_launch(const RmsArgs &a, RowLayout lay, int threads, cudaStream_t s) {
   return WAN_OK;
 }
 
+// Shared memory of a ragged row of D elements: each buffer with 16 bytes for the
+// row's offset in them.
+constexpr int ragged_buf(int D, int es) { return (D * es + 16 + 15) / 16 * 16; }
+
+// The long form may take more than the 48 KB (with its own 256 bytes) that a
+// kernel gets unasked. The limit belongs to the kernel and not to the call, so it
+// is raised once on a device, to what the widest row takes: raised to each call's
+// own size, it could be lowered by one host thread before another one's launch.
 template <typename XT, typename RT, bool RES, typename YT, int NV>
 int rms_launch_ragged(const RmsArgs &a, int threads, cudaStream_t s) {
   constexpr int es = sizeof(XT) > sizeof(YT) ? sizeof(XT) : sizeof(YT);
-  const int xb = (a.D * es + 16 + 15) / 16 * 16, rb = RES ? (a.D * (int)sizeof(RT) + 16 + 15) / 16 * 16 : 0;
-  if (xb + rb > 48 * 1024)
-    WAN_TRY_CUDA(cudaFuncSetAttribute(rmsnorm_ragged_kernel<XT, RT, RES, YT, NV>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, xb + rb), "rmsnorm smem attribute");
+  constexpr int widest = NV == RAGGED_NV ? RMS_MAX_D : RAGGED_SHORT_D;
+  constexpr int most = ragged_buf(widest, es) + (RES ? ragged_buf(widest, sizeof(RT)) : 0);
+  if constexpr (most > 48 * 1024 - 256) {
+    static std::atomic<uint64_t> ready{0};       // devices whose limit is raised
+    int dev = 0;
+    WAN_TRY_CUDA(cudaGetDevice(&dev), "rmsnorm device");
+    if (dev >= 64 || !(ready.load() >> dev & 1)) {
+      WAN_TRY_CUDA(cudaFuncSetAttribute(rmsnorm_ragged_kernel<XT, RT, RES, YT, NV>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, most), "rmsnorm smem attribute");
+      if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
+    }
+  }
+  const int xb = ragged_buf(a.D, es), rb = RES ? ragged_buf(a.D, sizeof(RT)) : 0;
   rmsnorm_ragged_kernel<XT, RT, RES, YT, NV><<<(unsigned)a.rows, threads, xb + rb, s>>>(a, xb);
   WAN_CHECK_LAUNCH("rmsnorm");
   return WAN_OK;
@@ -465,7 +485,7 @@ int rms_shape(const RmsArgs &a, RowLayout lay, cudaStream_t s) {
     if (n <= 1024) return rms_launch<XT, RT, RES, YT, 2, 0>(a, lay, threads(2), s);
     return rms_launch<XT, RT, RES, YT, 4, 0>(a, lay, threads(4), s);
   }
-  if (n <= 4096) return rms_launch_ragged<XT, RT, RES, YT, 8>(a, threads(8), s);
+  if (n <= RAGGED_SHORT_D) return rms_launch_ragged<XT, RT, RES, YT, 8>(a, threads(8), s);
   return rms_launch_ragged<XT, RT, RES, YT, RAGGED_NV>(a, threads(RAGGED_NV), s);
 }
 
