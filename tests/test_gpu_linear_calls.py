@@ -165,3 +165,17 @@ def test_rows_that_end_inside_16_bytes(M, N, res, out):
     assert (full[:, N:] == 7).all()
     c.check(o, list(range(0, M, max(1, M // 100))))
     assert wan.device_status() == wan.WAN_OK
+
+
+@pytest.mark.parametrize("M,N,K,f8", [(24, 13424, 2064, False), (32, 12072, 1552, False), (20, 12000, 4096, False),
+                                      (26, 12808, 4112, True), (29, 13504, 3000, False)])
+def test_few_tokens_three_ctas_to_an_sm(M, N, K, f8):
+    """17 to 32 tokens of so many weight rows that three CTAs share an SM and the
+    sums meet in the ring's memory; one call after another on a stream."""
+    c = Case(M, N, K, f8, "silu", res="bf16", out="f32")
+    first = c.run()
+    outs = [c.run() for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+    c.check(first)
+    assert wan.device_status() == wan.WAN_OK

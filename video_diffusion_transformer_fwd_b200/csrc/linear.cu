@@ -398,10 +398,15 @@ Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
   const int nkb = (num_k + c.split - 1) / c.split;
   const int nacc = accumulators_of(g, num_k, c), cols = columns_of(g, num_k, c);
   const int stage = stage_of(c);
-  // few tokens: a receive area of its own (at most 18 KB) saves a barrier after
-  // the products (14.6 -> 13.4 us at 1 x 5120 x 5120); more would cost stages
-  const int own = c.split > 1 && c.mt <= 32 ? recv_bytes(c) : 0;
-  int stages = (std::min(SM_SMEM / resident(g, num_k, c) - CTA_EXTRA, SMEM_MAX) - 1024 - own) / stage;
+  // few tokens: a receive area of its own (8 to 28 KB) saves a barrier after the
+  // products (14.6 -> 13.4 us at 1 x 5120 x 5120), unless it would leave the ring
+  // fewer than three stages, as it does for 17 to 32 tokens with three CTAs on an
+  // SM: 26 x 13304 x 11216 65.4 us with it and two stages, 59.2 without and with
+  // three, 20 x 12000 x 4096 22.0 and 21.2
+  const int room = std::min(SM_SMEM / resident(g, num_k, c) - CTA_EXTRA, SMEM_MAX) - 1024;
+  int own = c.split > 1 && c.mt <= 32 ? recv_bytes(c) : 0;
+  if ((room - own) / stage < std::min(3, nkb)) own = 0;
+  int stages = (room - own) / stage;
   stages = std::max(2, std::min(std::min(stages, nkb), MAX_STAGES));
   int smem = (own ? stages * stage + own : std::max(stages * stage, recv_bytes(c))) + 1024;
   smem = std::max(smem, cols > TMEM_SHARE ? SMEM_ALONE : SMEM_SHARE);
