@@ -567,9 +567,11 @@ int launch_plan(const LinArgs &g, const Plan &pl, cudaStream_t s) {
 }  // namespace
 
 int launch_linear(const LinArgs &g, cudaStream_t s) {
-  // the choice costs a few microseconds of the host: the last ones are kept, by
-  // all that it is made from (sizes, types, the rows' alignment, a residual)
+  // the choice costs a few microseconds of the host: it is kept in one of 32 slots,
+  // by all that it is made from (sizes, types, the rows' alignment, a residual, the
+  // card); sizes of one slot displace each other
   struct Known {
+    const Capacity *card;
     int M, N, K, kind;
     Choice choice;
   };
@@ -578,8 +580,9 @@ int launch_linear(const LinArgs &g, cudaStream_t s) {
   const int kind = 1 | (g.fp8 ? 2 : 0) | (g.out_f32 ? 4 : 0) | (e.vec_out && e.vec_res ? 8 : 0) | (g.res ? 16 : 0);
   const unsigned h = ((unsigned)g.M * 2654435761u ^ (unsigned)g.N * 40503u ^ (unsigned)g.K * 65599u ^ (unsigned)kind) >> 3;
   Known &k = known[h % 32];
-  if (k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
-    k = Known{g.M, g.N, g.K, kind, choose(g)};
+  const Capacity *card = &capacity();
+  if (k.card != card || k.M != g.M || k.N != g.N || k.K != g.K || k.kind != kind) {
+    k = Known{card, g.M, g.N, g.K, kind, choose(g)};
   }
   return k.choice.pair_bn ? gemm_tc_linear(g, k.choice.pair_bn, s) : launch_plan(g, k.choice.plan, s);
 }
