@@ -291,13 +291,8 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrive once on `bar_cluster` (this CTA's or the peer's mbarrier) when every
+// Arrive once on the mbarrier at this offset in both CTAs of the pair when every
 // tcgen05 op of the pair issued so far by this thread completes.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar_cluster) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               ::"r"(bar_cluster) : "memory");
-}
-// The same on the mbarrier at this offset in both CTAs of the pair.
 __device__ __forceinline__ void tc_commit_both(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                ::"r"(bar), "h"((uint16_t)3) : "memory");
