@@ -179,3 +179,28 @@ def test_few_tokens_three_ctas_to_an_sm(M, N, K, f8):
     assert all(torch.equal(first, o) for o in outs)
     c.check(first)
     assert wan.device_status() == wan.WAN_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(7, 1500, 4096), (24, 640, 5120), (48, 640, 5120), (333, 1003, 1000), (2304, 512, 640), (3000, 155, 2560)])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), 1e30])
+def test_rows_do_not_reach_each_other(M, N, K, f8, poison):
+    """Every third row of a call, when the other rows of a, of its scales and of
+    the residual turn into NaN, infinities or large values: the same bits."""
+    K = K // 16 * 16 if f8 else K
+    c = Case(M, N, K, f8, "silu", res="f32", out="f32")
+    before = c.run()
+    keep = torch.arange(0, M, 3, device="cuda")
+    others = torch.ones(M, device="cuda", dtype=torch.bool)
+    others[keep] = False
+    if f8:
+        c.a[others] = 127 if poison != 1e30 else 126            # NaN, or the largest code
+        c.sa[others] = poison
+    else:
+        c.a[others] = poison
+    c.r[others] = poison
+    after = c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(before[keep], after[keep]) and torch.isfinite(after[keep]).all()
+    assert not torch.equal(before[others], after[others])
+    assert wan.device_status() == wan.WAN_OK

@@ -60,3 +60,40 @@ def test_threads_with_rows_of_different_widths(out):
     for (_, _, _, want), out3 in zip(calls, got):
         assert all(torch.equal(a, b) for a, b in zip(want, out3) if a is not None)
     assert wan.device_status() == wan.WAN_OK
+
+
+@pytest.mark.parametrize("D,pad", [(128, 0), (1003, 0), (1000, 5), (5120, 0), (9000, 1)])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+def test_rows_do_not_reach_each_other(D, pad, poison):
+    """Every third row of a call, when the other rows of x and of the residual
+    turn into NaN or infinities: the same bits (aligned rows, rows off a boundary
+    and rows whose strides do not agree)."""
+    x, r, g = make(31, D)
+    wide = torch.zeros(31, D + pad, device="cuda", dtype=x.dtype)
+    wide[:, :D] = x
+    for out in ("bf16", "f32", "fp8"):
+        before = wan.rmsnorm(wide[:, :D], g, residual=r, out_dtype=out)
+        x2, r2 = wide.clone(), r.clone()
+        others = torch.ones(31, device="cuda", dtype=torch.bool)
+        others[::3] = False
+        x2[others], r2[others] = poison, poison
+        after = wan.rmsnorm(x2[:, :D], g, residual=r2, out_dtype=out)
+        for a, b in zip(before, after):
+            assert a is None or torch.equal(a[::3], b[::3])
+
+
+def test_captured_before_any_call_at_these_widths():
+    """Kernels that no call has launched yet, captured: rows of every layout."""
+    xs = [make(5, D, "f32", "bf16", seed=D) for D in (24, 90, 200, 450, 700, 2100, 8500)]
+    wide = torch.randn(5, 5001, device="cuda")
+    outs = []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for x, r, g in xs:
+            outs.append(wan.rmsnorm(x, g, residual=r, out_dtype="bf16"))
+        outs.append(wan.rmsnorm(wide[:, :5000], None, out=torch.empty(5, 5000, device="cuda")))
+    graph.replay()
+    torch.cuda.synchronize()
+    for (x, r, g), (y, s, h) in zip(xs, outs):
+        check(x, r, g, "bf16", y, s, h)
+    check(wide[:, :5000], None, None, "f32", *outs[-1])
