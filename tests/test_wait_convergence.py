@@ -1,4 +1,4 @@
-"""Bounded waits of the kernels and lanes that leave their warp, read from their sources (no GPU needed).
+"""Waits of the kernels and lanes that leave their warp, read from the sources (no GPU needed).
 
 mbar_wait answers each thread for itself, so the lanes of a warp may leave one
 at the end of its limit with different answers. The instructions that follow in
@@ -66,3 +66,13 @@ def test_no_lane_leaves_its_warp(name):
     with open(os.path.join(CSRC, name)) as f:
         text = plain(f.read())
     assert re.findall(r"if \([^;{}]*\b(?:lane|threadIdx\.x)\b[^;{}]*\) (?:return|break|continue)\b", text) == []
+
+
+def test_no_cta_waits_for_tmem_of_another():
+    """Kernels that take more of TMEM than a share take the shared memory that
+    keeps other CTAs off their SM."""
+    for name in SOURCES:
+        with open(os.path.join(CSRC, name)) as f:
+            text = plain(f.read())
+        if "tmem_alloc" in text:
+            assert "SMEM_ALONE" in text, name

@@ -45,6 +45,7 @@ constexpr uint32_t IDESC_S = idesc_bf16(TQ, TK, 0);
 constexpr uint32_t IDESC_O = idesc_bf16(TQ, D, 1);
 constexpr float RESCALE_THRESHOLD = 8.0f;   // log2 units
 constexpr int SMEM_BYTES = 1024 + 4 * TILE_BYTES + NSLOT * TILE_BYTES + 256;   // Q_0, Q_1, P_0, P_1, ring
+static_assert(SMEM_BYTES >= SMEM_ALONE, "all of TMEM");
 
 struct FaParams {
   int B, heads, Lq, Lk;

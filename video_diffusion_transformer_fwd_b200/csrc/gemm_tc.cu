@@ -75,6 +75,7 @@ struct Geo {
   static constexpr int SMEM_BYTES = LIN ? 232448 : 1024 + STAGES * STAGE_BYTES + EPI_SMEM + 256;
   static_assert(!(WIDE && LIN), "wan_linear runs the narrow tile");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+  static_assert(SMEM_BYTES >= SMEM_ALONE, "all of TMEM");
   static_assert(8 * (2 * STAGES + 4) + 16 + 8 * EPI_WARPS <= 256, "barriers");
   static_assert(NACC * BN <= (int)TMEM_COLS, "TMEM columns");
 };

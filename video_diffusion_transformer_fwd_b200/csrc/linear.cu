@@ -343,7 +343,7 @@ struct Plan {
   int stages, smem, chunk, tmem_cols, recv;
 };
 
-constexpr int SM_SMEM = 228 * 1024, CTA_EXTRA = 1024 + 256;     // of an SM; what a CTA takes besides its ring
+constexpr int CTA_EXTRA = 1024 + 256;                          // shared memory that a CTA takes besides its ring
 constexpr int SMS = 148;
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
@@ -368,20 +368,15 @@ int ctas_per_sm(const LinArgs &g, const Cut &c) {
   const int room = capacity().clusters[c.split];
   return (int)((clusters + room - 1) / room);
 }
-// TMEM columns that a CTA has without asking for more than its share
-constexpr int TMEM_SHARE = 128;
 // Accumulators of a CTA: one for every part of its K (lin_parts), as many as go
 // into its share of TMEM while a part then stays below 16 steps, else into all of it
 int accumulators_of(const LinArgs &g, int num_k, const Cut &c) {
   const int nkb = (num_k + c.split - 1) / c.split, want = lin_parts(g, nkb), share = TMEM_SHARE / c.mt;
   return std::min(want, nkb <= 16 * share ? share : 512 / c.mt);
 }
-// TMEM columns. CTAs of a cluster wait for one another, so none may wait for
-// TMEM that a CTA of another cluster holds on the same SM. So a CTA takes 128
-// columns, in one size for no gaps between them, and at least a quarter of the
-// SM's shared memory with them, or more columns, and then so much shared memory
-// that no other one fits beside it.
-constexpr int SMEM_SHARE = SM_SMEM / 4 - CTA_EXTRA, SMEM_ALONE = SM_SMEM - SM_SMEM / 4;
+// TMEM columns of a CTA, and the shared memory that goes with its share of them
+// (sm100.cuh, SMEM_ALONE)
+constexpr int SMEM_SHARE = SM_SMEM / 4 - CTA_EXTRA;
 int columns_of(const LinArgs &g, int num_k, const Cut &c) {
   int cols = TMEM_SHARE;
   while (cols < accumulators_of(g, num_k, c) * c.mt) cols *= 2;

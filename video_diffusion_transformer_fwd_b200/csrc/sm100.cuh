@@ -167,6 +167,16 @@ __device__ __forceinline__ void bulk_wait_group_read() {
 __device__ __forceinline__ void bulk_wait_group_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- tcgen05
+// TMEM on an SM that CTAs of several kernels share. tcgen05.alloc waits until the
+// columns are free, and CTAs of a cluster wait for one another: two clusters could
+// each hold columns on one SM and wait for columns, behind another CTA's alloc, on
+// the next. So no alloc ever waits: a CTA takes TMEM_SHARE columns in one size (no
+// gaps between them) and at least a quarter of the SM's shared memory, or more
+// columns, and then dynamic shared memory of SMEM_ALONE at least, beside which no
+// CTA of either kind fits.
+constexpr int SM_SMEM = 228 * 1024;            // shared memory of an SM
+constexpr int TMEM_SHARE = 128;
+constexpr int SMEM_ALONE = SM_SMEM - SM_SMEM / 4;
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                ::"r"(dst_smem), "r"(ncols) : "memory");
