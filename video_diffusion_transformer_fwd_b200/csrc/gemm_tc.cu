@@ -498,18 +498,21 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int a_row = mb * 2 * BM + (int)rank * BM;
       const int b_row = n0 - seg * p.segN + (int)rank * (LIN ? BN / 2 : 128);   // this CTA's rows of each N = 256 half (of bn)
       for (int kb = 0; kb < p.num_k; ++kb) {
-        mbar_wait_lanes(ok, smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101);
-        if (elect_one() && ok) {
-          const uint32_t fb_local = smem_u32(&full[stage]);
-          if (leader) mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
-          const uint32_t fb = mapa_shared(fb_local, 0);
-          const int kx = kb * (F8 ? BK8 : BK);
-          tma_load_2d_pair(smem_u32(sA + stage * A_BYTES), &tmA, kx, a_row, fb);
-          tma_load_2d_pair(smem_u32(sB + stage * B_BYTES), bm, kx, b_row, fb);
-          if (WIDE)      // the second N = 256 half of the tile: B rows 256 further
-            tma_load_2d_pair(smem_u32(sB + stage * B_BYTES + B_BYTES / 2), bm, kx, b_row + 256, fb);
+        if (!LIN) mbar_wait_lanes(ok, smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101);
+        if (elect_one()) {         // ok and loads that count are this thread's
+          if (LIN) ok = ok && mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.watchdog, 0x101);
+          if (ok) {
+            const uint32_t fb_local = smem_u32(&full[stage]);
+            if (leader) mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
+            const uint32_t fb = mapa_shared(fb_local, 0);
+            const int kx = kb * (F8 ? BK8 : BK);
+            tma_load_2d_pair(smem_u32(sA + stage * A_BYTES), &tmA, kx, a_row, fb);
+            tma_load_2d_pair(smem_u32(sB + stage * B_BYTES), bm, kx, b_row, fb);
+            if (WIDE)      // the second N = 256 half of the tile: B rows 256 further
+              tma_load_2d_pair(smem_u32(sB + stage * B_BYTES + B_BYTES / 2), bm, kx, b_row + 256, fb);
+            ++loads;
+          }
         }
-        if (ok) ++loads;
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     }
@@ -540,27 +543,35 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           const uint32_t d = tmem_base + buf * buf_cols;
           const int kb0 = LIN ? part * p.part_steps : 0, kb1 = LIN ? min(p.num_k, kb0 + p.part_steps) : p.num_k;
           for (int kb = kb0; kb < kb1; ++kb) {
-            mbar_wait_lanes(ok, smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112);
-            tc_fence_after();
+            if (!LIN) {
+              mbar_wait_lanes(ok, smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112);
+              tc_fence_after();
+            }
             const int first = kb - kb0;
             const uint64_t a0 = desc_kmajor_sw128(smem_u32(sA + stage * A_BYTES));
             const uint64_t b0 = desc_kmajor_sw128(smem_u32(sB + stage * B_BYTES));
             // 4 MMAs of 32 bytes of K per stage (16 bf16 or 32 e4m3 each):
             // the descriptor start address advances 32 bytes (2 in 16-byte units)
-            if (elect_one() && ok) {
-#pragma unroll
-              for (int h = 0; h < G::BN / 256; ++h) {
-                // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
-                const uint64_t bh = b0 + (uint64_t)((h * (B_BYTES / 2)) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk) {
-                  if (F8)
-                    mma_ss_pair_f8(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (first | kk) != 0);
-                  else
-                    mma_ss_pair(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (first | kk) != 0);
-                }
+            if (elect_one()) {
+              if (LIN) {
+                ok = ok && mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.watchdog, 0x112);
+                tc_fence_after();
               }
-              tc_commit_both(smem_u32(&empty[stage]));
+              if (ok) {
+#pragma unroll
+                for (int h = 0; h < G::BN / 256; ++h) {
+                  // N = 256 half h: B rows of this half at + h * B_BYTES / 2, accumulator columns + 256 h
+                  const uint64_t bh = b0 + (uint64_t)((h * (B_BYTES / 2)) >> 4);
+#pragma unroll
+                  for (int kk = 0; kk < BK / 16; ++kk) {
+                    if (F8)
+                      mma_ss_pair_f8(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC8, (first | kk) != 0);
+                    else
+                      mma_ss_pair(d + 256 * h, a0 + 2 * kk, bh + 2 * kk, LIN ? p.idesc : IDESC, (first | kk) != 0);
+                  }
+                }
+                tc_commit_both(smem_u32(&empty[stage]));
+              }
             }
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
           }

@@ -84,19 +84,25 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // mbar_wait is for one thread: of two lanes at the end of a wait one may give up
 // and the other see the phase complete. What follows in a warp (elect.sync,
 // tcgen05.ld, __syncwarp) waits for every lane, without a limit, so the lanes
-// have to go on together or stop together. A warp therefore waits in one of two
-// ways. mbar_wait_warp: one answer for all lanes, by a vote.
+// have to go on together or stop together. A warp therefore waits by its elected
+// thread alone, or in one of two ways. mbar_wait_warp: one answer for all lanes,
+// by a vote.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, int *watchdog,
                                                int code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, watchdog, code));
 }
 
 // mbar_wait_lanes: a lane that gives up clears its own `ok` and goes on beside
-// the others, without waiting any more. Loops that run in all lanes for the sake
-// of one that issues (elect_one) wait so: they end by their counts alone, and a
-// step is issued where the elected lane, the same one every time, is still ok.
-// (A vote at every step costs wan_linear's split kernel more: 333 x 1003 x 1000
-// 9.1 us, 8.7 this way.)
+// the others, without waiting any more.
+//
+// Loops that run in all lanes for the sake of one that issues (elect_one) end by
+// their counts alone, and a step is issued where the elected lane, the same one
+// every time, is still ok. Which thread waits is measured: with mbar_wait_lanes the
+// block GEMM (1.3B block at L = 7800 0.590 ms of products; the elected thread alone
+// 0.594) and wan_linear's split kernel, which asks for the next step ahead of the
+// current one's issue (333 x 1003 x 1000 8.7 us; the elected thread alone 9.0, a vote
+// at every step 9.1); by the elected thread alone wan_linear on CTA pairs (2560 x
+// 1536 x 8960 onto float32 74.1 us; mbar_wait_lanes 76.2).
 __device__ __forceinline__ void mbar_wait_lanes(bool &ok, uint32_t bar, uint32_t parity, volatile int *abort,
                                                 int *watchdog, int code) {
   if (ok && !mbar_wait(bar, parity, abort, watchdog, code)) ok = false;
@@ -111,8 +117,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 }
 
 // One thread of a converged warp. A loop that issues TMA or tcgen05 work runs in
-// all lanes with only the issue itself under elect_one(): its operands then
-// stay in uniform registers. Inside `if (lane == 0)` each of them is moved
+// all lanes with only the issue (and its wait) under elect_one(): its operands
+// then stay in uniform registers. Inside `if (lane == 0)` each of them is moved
 // there lane by lane (four tcgen05.mma took 224 cycles to issue, 99 this way).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
