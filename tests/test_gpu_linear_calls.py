@@ -204,3 +204,14 @@ def test_rows_do_not_reach_each_other(M, N, K, f8, poison):
     assert torch.equal(before[keep], after[keep]) and torch.isfinite(after[keep]).all()
     assert not torch.equal(before[others], after[others])
     assert wan.device_status() == wan.WAN_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1024, 13824), (24, 520, 13824), (100, 384, 8192), (300, 640, 2048), (2304, 1003, 2048), (2500, 512, 13824)])
+def test_float32_output_loses_no_more_than_a_part(M, N, K):
+    """The tensor core's rounding toward zero counts 1.1e-9 for each element of K
+    of a part, and a part has 2048 at most: 2.3e-6 of the product's norm, and the
+    float32 additions of its parts (14 at most, 2^-24 each)."""
+    c = Case(M, N, K, bias=False, out="f32")
+    want = c.a.double() @ c.w.double().t()
+    err = float((c.run().double() - want).norm() / want.norm())
+    assert err <= 2.3e-6 + 14 * 2.0 ** -24, err

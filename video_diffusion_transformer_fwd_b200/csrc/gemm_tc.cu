@@ -134,10 +134,11 @@ __device__ __forceinline__ float bf16_bits_to_float(uint32_t lo16) {
 // tiles of the warp (float32: 128-byte rows, 16-byte group g of row r at
 // g ^ (r & 7); bf16: 64-byte rows, at g ^ (r / 2 & 3)) and the TMA unit, which
 // keeps the warp's own loads and stores to shared memory: a version that stored
-// rows of 32 bytes from registers held the 7800 x 8960 x 1536 product at 182 us,
-// which is now at 150 (1.43 PFLOP/s), its products alone at 141. The residual of a chunk is asked for when the
-// chunk before it has been added, the first one of a tile during the last of
-// the tile before. Outputs (or residuals) whose rows do not start on 16-byte
+// rows of 32 bytes from registers held the 7800 x 8960 x 1536 product at 182 us
+// in a captured graph, where it is now at 152 (1.41 PFLOP/s), its products alone at
+// 141; call after call, under the power cap, it takes 182 (1.18). The residual of a
+// chunk is asked for when the chunk before it has been added, the first one of a
+// tile during the last of the tile before. Outputs (or residuals) whose rows do not start on 16-byte
 // boundaries, and the last chunk of rows that end inside 16 bytes, are turned
 // around in shared memory instead and stored a column per lane.
 template <bool F8>

@@ -26,10 +26,12 @@
 // and on CTA pairs, whose CTAs fill an SM, it cost time: 93600 x 128 10.7 ->
 // 13.2 us, 512 x 5120 x 4096 32.8 -> 33.2.)
 //
-// Measured: 1 x 5120 x 5120 bf16 12.9 us (4.1 TB/s of weights; 8.0 at the copy's
-// rate, and a launch is 2.4), 24 x 13824 x 5120 e4m3 16.6 us (4.3 TB/s), 333 x
-// 1003 x 1000 8.8 us, which is a launch, one trip to memory, the sums' exchange
-// and the epilogue.
+// Measured (in a captured graph and call after call alike): 1 x 5120 x 5120 bf16
+// 12.8 us (4.1 TB/s of weights; 8.0 at the copy's rate, and a launch is 2.6), 24 x
+// 13824 x 5120 e4m3 16.4 us (4.3 TB/s), 333 x 1003 x 1000 8.7 us. Library products
+// of these sizes take 11.7, 14.1 and 4.7. Whole CTAs fall on the SMs: the 240 CTAs of
+// the first leave the longest SM 23% more steps than the mean, the 216 of the second
+// 37%. The third is a launch, one trip to memory, the sums' exchange and the epilogue.
 #include "common.cuh"
 #include "linear.cuh"
 #include "sm100.cuh"
@@ -415,7 +417,9 @@ Plan make_plan(const LinArgs &g, int num_k, const Cut &c) {
 // HBM for the first tile that reads it), and the card 3400 from HBM; SM and CTAs
 // need 400 cycles for a step of K at least; a token costs the epilogue 45, 70
 // with a residual. The cut or pair tile taken by these two costs was 1 to 3%
-// slower in the mean than the best of all, over four sets of 26 random sizes.
+// slower in the mean than the best of all, over six sets of 26 random sizes; the
+// worst of the last 52 by 37% (735 x 2052 x 592: pair tiles 11.7 us, tiles of 48
+// tokens 8.5), four more by 5 to 15%.
 double split_cost(const LinArgs &g, int num_k, const Cut &c) {
   const double ntn = (g.N + WROWS - 1) / WROWS, ntm = (g.M + c.mt - 1) / c.mt;
   const double per_sm = ctas_per_sm(g, c);

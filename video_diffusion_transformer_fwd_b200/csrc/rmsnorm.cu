@@ -26,9 +26,10 @@
 //                          memory, where its elements are picked at their own
 //                          offsets (12000 x 3163 bf16: 82 us, 42 where the
 //                          strides agree).
-// Measured: 32760 x 5120 bf16 onto a float32 stream and into codes 262 us (7.0
-// TB/s), 7800 x 1536 of the same 21.8 (6.0), 93600 x 128 bf16 10.6 (4.5), 2011 x
-// 1037 7.4 (2.8), one row of 5120 2.4 us, which is a launch. Short calls are
+// Measured in a captured graph: 32760 x 5120 bf16 onto a float32 stream and into
+// codes 264 us (7.0 TB/s; call after call 288, 6.4), 7800 x 1536 of the same 21.9
+// (6.0; 22.9), 93600 x 128 bf16 10.4 (4.6; 12.0), 2011 x 1037 6.6 (3.2; 8.2), one row
+// of 5120 2.6 us, which is a launch (8.1: the host's work). Short calls are
 // bound by the launch and one trip to memory; dense rows of odd width by the
 // instructions that pick their elements.
 #include "common.cuh"

@@ -458,6 +458,7 @@ def rmsnorm(x, gain=None, residual=None, eps=1e-6, out_dtype=None, out=None, row
     ``out_dtype`` is "bf16", "f32" or "fp8" (e4m3 codes, uint8, with one
     float32 scale per row); by default the type of ``out``, or of x. Outputs
     that are not given are allocated. Rows may be strided (2-D tensors).
+    Forward only: no gradient is recorded.
     Returns (y, row_scale, h): row_scale is None unless y holds codes, h is x
     itself without a residual and has the residual's type with one."""
     torch, codes = _torch(), _Types.codes or _Types.get()
@@ -516,7 +517,8 @@ def linear(a, w, bias=None, activation="none", residual=None, a_scale=None, w_sc
     or "relu"; residual [..., N] bf16 or float32 and may be ``out`` itself.
     ``out_dtype`` is "bf16" or "f32" (by default the type of ``out``, of the
     residual, or bf16). Rows may be strided (2-D tensors); those of a and w
-    start on 16-byte boundaries. Returns out [..., N]."""
+    start on 16-byte boundaries. Forward only: no gradient is recorded.
+    Returns out [..., N]."""
     torch, codes = _torch(), _Types.codes or _Types.get()
     dev = a.get_device()
     if dev < 0:
