@@ -27,7 +27,7 @@
 // 13.2 us, 512 x 5120 x 4096 32.8 -> 33.2.)
 //
 // Measured (in a captured graph and call after call alike): 1 x 5120 x 5120 bf16
-// 12.8 us (4.1 TB/s of weights; 8.0 at the copy's rate, and a launch is 2.6), 24 x
+// 12.7 us (4.1 TB/s of weights; 8.0 at the copy's rate, and a launch is 2.5), 24 x
 // 13824 x 5120 e4m3 16.4 us (4.3 TB/s), 333 x 1003 x 1000 8.7 us. Library products
 // of these sizes take 11.7, 14.1 and 4.7. Whole CTAs fall on the SMs: the 240 CTAs of
 // the first leave the longest SM 23% more steps than the mean, the 216 of the second

@@ -26,10 +26,11 @@
 //                          memory, where its elements are picked at their own
 //                          offsets (12000 x 3163 bf16: 82 us, 42 where the
 //                          strides agree).
-// Measured in a captured graph: 32760 x 5120 bf16 onto a float32 stream and into
-// codes 264 us (7.0 TB/s; call after call 288, 6.4), 7800 x 1536 of the same 21.9
-// (6.0; 22.9), 93600 x 128 bf16 10.4 (4.6; 12.0), 2011 x 1037 6.6 (3.2; 8.2), one row
-// of 5120 2.6 us, which is a launch (8.1: the host's work). Short calls are
+// Measured in a captured graph, inputs out of L2 (call after call): 32760 x 5120
+// bf16 onto a float32 stream and into codes 264 us, 7.0 TB/s (288), 7800 x 1536 of
+// the same 22.4, 5.9 TB/s (22.9), 93600 x 128 bf16 10.6, 4.5 TB/s (12.0), 2011 x 1037
+// 7.4, 2.8 TB/s (8.2), one row of 5120 2.5 us, which is a launch (8.1: the host's
+// work). Short calls are
 // bound by the launch and one trip to memory; dense rows of odd width by the
 // instructions that pick their elements.
 #include "common.cuh"
